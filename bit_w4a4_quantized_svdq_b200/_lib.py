@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, Structure, c_char_p, c_int, c_int64, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, Structure, c_char_p, c_float, c_int, c_int64, c_size_t, c_uint32, c_void_p
 
 from .build import DEBUG_LIB_PATH, LIB_PATH
 
@@ -77,6 +77,16 @@ SIGNATURES = {
     "svdq_quantize_mxfp8": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
     "svdq_linear_mxfp8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64,
                                   c_int64, c_int64, c_void_p]),
+    "svdq_mxfp4_sf_bytes": (c_size_t, [c_int64, c_int64]),
+    "svdq_quantize_mxfp4": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
+    "svdq_dequantize_mxfp4": (c_int, [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p]),
+    "svdq_dequantize_mxfp8": (c_int, [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p]),
+    "svdq_linear_mxfp4": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64,
+                                  c_int64, c_int64, c_void_p]),
+    "svdq_rmsnorm_mxfp8": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_int, c_float,
+                                   c_void_p, c_int64, c_void_p, c_void_p, c_void_p]),
+    "svdq_rmsnorm_mxfp4": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_int, c_float,
+                                   c_void_p, c_int64, c_void_p, c_void_p, c_void_p]),
 }
 
 _lib = None

@@ -21,7 +21,8 @@ DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libsvdq_debug.so")
 VARIANT_FLAGS = {LIB_PATH: [], DEBUG_LIB_PATH: ["-DSVDQ_DEBUG_CHECKS=1"]}
 INCLUDE = os.path.join(os.path.dirname(PKG_DIR), "include")
 
-SOURCES = ["abi.cu", "calib.cu", "quantize.cu", "linear.cu", "score.cu", "residual.cu", "proxy.cu", "grid.cu", "mxfp8.cu"]
+SOURCES = ["abi.cu", "calib.cu", "quantize.cu", "linear.cu", "score.cu", "residual.cu", "proxy.cu", "grid.cu", "mxfp8.cu",
+           "mxfp4.cu", "rmsnorm.cu", "linear_mx4.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",

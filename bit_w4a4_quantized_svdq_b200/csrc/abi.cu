@@ -33,11 +33,11 @@ EncodeTiledFn g_encode = nullptr;
 int current_device_index() { return current_device(); }
 
 // Armed extent limits + 1 per store site (0: none armed).
-std::atomic<int64_t> g_extent_limit[kSiteCount] = {};
+std::atomic<int64_t> g_extent_limit[kSiteEnd] = {};
 
 int64_t debug_extent(uint32_t site, int64_t extent) {
 #if SVDQ_DEBUG_CHECKS
-    if (site < kSiteCount) {
+    if (store_site_known(static_cast<int>(site))) {
         const int64_t lim = g_extent_limit[site].exchange(0, std::memory_order_acq_rel) - 1;
         if (lim >= 0 && lim < extent) return lim;
     }
@@ -192,7 +192,7 @@ int svdq_debug_build(void) { return SVDQ_DEBUG_CHECKS ? 1 : 0; }
 
 int svdq_debug_limit_extent(int site, int64_t extent) {
 #if SVDQ_DEBUG_CHECKS
-    if (site < 1 || site >= static_cast<int>(svdq::kSiteCount) || extent < 0) return SVDQ_ERR_INVALID_ARG;
+    if (!svdq::store_site_known(site) || extent < 0) return SVDQ_ERR_INVALID_ARG;
     svdq::g_extent_limit[site].store(extent + 1, std::memory_order_release);
     return SVDQ_OK;
 #else

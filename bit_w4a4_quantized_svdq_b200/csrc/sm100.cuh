@@ -58,8 +58,19 @@ enum StoreSite : uint32_t {
     kSiteBits = 14,           // bits lost
     kSiteMxCodes = 15,        // MXFP8 quantiser: codes
     kSiteMxSf = 16,           // MXFP8 quantiser: scale bytes
-    kSiteCount = 17
+    kSiteCount = 17,
+    // Numbered apart from the sites above.
+    kSiteNormH = 32,          // RMS norm: the sum of input and residual
+    kSiteMxValues = 33,       // MX read-back: bf16 values
+    kSiteLinearMx4 = 34,      // MXFP4 linear: plain stores of Y
+    kSiteEnd = 35
 };
+
+// The sites a test may arm.
+constexpr bool store_site_known(int site) {
+    return (site >= 1 && site < static_cast<int>(kSiteCount)) ||
+           (site >= static_cast<int>(kSiteNormH) && site < static_cast<int>(kSiteEnd));
+}
 
 // A store of `width` elements at element offset `off` into an output of
 // `extent` elements.
@@ -356,6 +367,19 @@ __device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint6
            "r"(sfa_tmem), "r"(sfb_tmem) : "memory");
 }
 
+// Block-scaled FP4 MMA: kind::mxf4, E2M1 inputs, one E8M0 scale per 32 elements,
+// K = 64 per instruction.  Each 32-bit tensor-memory scale word holds four scale
+// bytes; the instruction descriptor's scale ids (0 or 2) pick the pair.
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+        :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate),
+           "r"(sfa_tmem), "r"(sfb_tmem) : "memory");
+}
+
 // Copy a 32-row x 128-bit shared-memory block into tensor memory, replicated
 // into all four 32-lane quarters (the layout block scales are read from).
 __device__ __forceinline__ void tc_cp_32x128b_x4(uint32_t taddr, uint64_t sdesc) {
@@ -381,6 +405,13 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
         : "r"(taddr));
 }
 
@@ -446,6 +477,13 @@ __device__ __forceinline__ void tmem_ld_tie(uint32_t (&r)[16]) {
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_tie(uint32_t (&r)[8]) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[N]) {
     tmem_ld_wait();
@@ -471,6 +509,19 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 
 __device__ __forceinline__ void pdl_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Address of `p` (this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // Full cluster barrier (every thread of every CTA of the cluster).
@@ -530,6 +581,19 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(uint32_t m, uint32_t n, uint32
     return (sf_id << 4)         // B scale factor id
          | (0u << 7)            // A format: E4M3
          | (0u << 10)           // B format: E4M3
+         | ((n >> 3) << 17)     // N / 8
+         | (1u << 23)           // scale format: E8M0
+         | ((m >> 4) << 24)     // M / 16
+         | (sf_id << 29);       // A scale factor id
+}
+
+// Instruction descriptor, kind::mxf4 with E2M1 A/B and E8M0 block scales (one per
+// 32 elements), both K-major, K = 64 per instruction; `sf_id` (0 or 2) selects the
+// byte pair of the A and B scale words this instruction uses.
+__host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t m, uint32_t n, uint32_t sf_id) {
+    return (sf_id << 4)         // B scale factor id
+         | (1u << 7)            // A format: E2M1
+         | (1u << 10)           // B format: E2M1
          | ((n >> 3) << 17)     // N / 8
          | (1u << 23)           // scale format: E8M0
          | ((m >> 4) << 24)     // M / 16

@@ -432,6 +432,137 @@ def svdq_linear_mxfp8(a_codes: torch.Tensor, a_sf: torch.Tensor, w_codes: torch.
     return out
 
 
+def mxfp4_sf_bytes(rows: int, k: int) -> int:
+    return int(_lib.load().svdq_mxfp4_sf_bytes(rows, k))
+
+
+def _mx_outputs(out: Optional[dict], m: int, k: int, code_cols: int, dev) -> dict:
+    """Codes [m, code_cols] and scale bytes of a microscaled quantiser: the caller's, checked, or new ones."""
+    nbytes = mxfp8_sf_bytes(m, k)
+    if nbytes == 0:
+        raise ValueError("K must be a positive multiple of 128 and M at least 1")
+    if out is None:
+        out = dict(codes=_lib.out_empty((m, code_cols), torch.uint8, dev), sf=_lib.out_empty(nbytes, torch.uint8, dev))
+    _check_dense(out["codes"], (torch.uint8,), m * code_cols, "out['codes']")
+    _check_dense(out["sf"], (torch.uint8,), nbytes, "out['sf']")
+    return out
+
+
+@_on_tensor_device
+def svdq_quantize_mxfp4(x: torch.Tensor, out: Optional[dict] = None, stream=None) -> dict:
+    """bf16 [M, K] -> dict(codes u8 [M, K/2] packed E2M1, sf u8 E8M0 scales in the tensor-core layout)."""
+    lib = _lib.load()
+    _check_bf16(x, "x")
+    m, k = x.shape
+    out = _mx_outputs(out, m, k, k // 2, x.device)
+    _lib.check("svdq_quantize_mxfp4", lib.svdq_quantize_mxfp4(
+        _ptr(x), m, k, _row_stride(x, "x"), _ptr(out["codes"]), _ptr(out["sf"]), _stream(stream)))
+    return out
+
+
+def _dequantize_mx(name: str, codes: torch.Tensor, sf: torch.Tensor, per_byte: int, out, stream) -> torch.Tensor:
+    lib = _lib.load()
+    if codes.dim() != 2:
+        raise ValueError("codes must be a 2-D byte tensor")
+    m, k = codes.shape[0], codes.shape[1] * per_byte
+    nbytes = mxfp8_sf_bytes(m, k)
+    if nbytes == 0:
+        raise ValueError("K must be a positive multiple of 128 and M at least 1")
+    _check_dense(codes, (torch.uint8,), 0, "codes")
+    _check_dense(sf, (torch.uint8,), nbytes, "sf")
+    if out is None:
+        out = _lib.out_empty((m, k), torch.bfloat16, codes.device)
+    if out.dtype not in _BF16_TYPES or tuple(out.shape) != (m, k):
+        raise ValueError(f"out must be a bf16 [{m}, {k}] tensor")
+    _lib.check(name, getattr(lib, name)(_ptr(codes), _ptr(sf), m, k, _ptr(out), _row_stride(out, "out"),
+                                        _stream(stream)))
+    return out
+
+
+@_on_tensor_device
+def svdq_dequantize_mxfp4(codes: torch.Tensor, sf: torch.Tensor, out: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """Values of MXFP4 codes u8 [M, K/2] and their scales: bf16 [M, K]."""
+    return _dequantize_mx("svdq_dequantize_mxfp4", codes, sf, 2, out, stream)
+
+
+@_on_tensor_device
+def svdq_dequantize_mxfp8(codes: torch.Tensor, sf: torch.Tensor, out: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """Values of MXFP8 codes u8 [M, K] and their scales: bf16 [M, K]."""
+    return _dequantize_mx("svdq_dequantize_mxfp8", codes, sf, 1, out, stream)
+
+
+@_on_tensor_device
+def svdq_linear_mxfp4(a_codes: torch.Tensor, a_sf: torch.Tensor, w_codes: torch.Tensor, w_sf: torch.Tensor,
+                      bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """Y bf16 [M, N] = dequant(A) dequant(W)^T + bias on the MXFP4 tensor-core path."""
+    lib = _lib.load()
+    if a_codes.dim() != 2 or w_codes.dim() != 2:
+        raise ValueError("a_codes and w_codes must be 2-D [rows, K/2] byte tensors")
+    m, kh = a_codes.shape
+    n, k = w_codes.shape[0], 2 * kh
+    _check_matrix(a_codes, (torch.uint8,), m, kh, "a_codes")
+    _check_matrix(w_codes, (torch.uint8,), n, kh, "w_codes")
+    _check_dense(a_sf, (torch.uint8,), mxfp4_sf_bytes(m, k), "a_sf")
+    _check_dense(w_sf, (torch.uint8,), mxfp4_sf_bytes(n, k), "w_sf")
+    _check_dense(bias, _BF16_TYPES, n, "bias", optional=True)
+    if out is None:
+        out = _lib.out_empty((m, n), torch.bfloat16, a_codes.device)
+    if out.dtype not in _BF16_TYPES or tuple(out.shape) != (m, n):
+        raise ValueError(f"out must be a bf16 [{m}, {n}] tensor")
+    _lib.check("svdq_linear_mxfp4", lib.svdq_linear_mxfp4(
+        _ptr(a_codes), _ptr(a_sf), _ptr(w_codes), _ptr(w_sf), _ptr(bias), _ptr(out), _row_stride(out, "out"),
+        m, n, k, _stream(stream)))
+    return out
+
+
+def _rmsnorm_mx(name: str, x, weight, residual, eps: float, per_byte: int, out, stream) -> dict:
+    lib = _lib.load()
+    _check_bf16(x, "x")
+    m, k = x.shape
+    _check_dense(weight, (torch.bfloat16, torch.float32), 0, "weight")
+    if weight.numel() != k:
+        raise ValueError(f"weight holds {weight.numel()} elements, a row of x {k}")
+    if residual is not None:
+        _check_bf16(residual, "residual")
+        if tuple(residual.shape) != (m, k):
+            raise ValueError(f"residual must be [{m}, {k}], got {list(residual.shape)}")
+    h = None if out is None else out.get("h")
+    codes = _mx_outputs(out, m, k, k // per_byte, x.device)
+    if residual is None:
+        if h is not None:
+            raise ValueError("out['h'] is the sum with a residual, and there is none")
+    elif h is None:
+        h = _lib.out_empty((m, k), torch.bfloat16, x.device)
+    if h is not None and (h.dtype not in _BF16_TYPES or tuple(h.shape) != (m, k)):
+        raise ValueError(f"out['h'] must be a bf16 [{m}, {k}] tensor")
+    _lib.check(name, getattr(lib, name)(
+        _ptr(x), m, k, _row_stride(x, "x"), _ptr(residual),
+        0 if residual is None else _row_stride(residual, "residual"), _ptr(weight),
+        1 if weight.dtype == torch.float32 else 0, float(eps), _ptr(h), 0 if h is None else _row_stride(h, "out['h']"),
+        _ptr(codes["codes"]), _ptr(codes["sf"]), _stream(stream)))
+    return dict(codes=codes["codes"], sf=codes["sf"], h=h)
+
+
+@_on_tensor_device
+def svdq_rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                       eps: float = 1e-6, out: Optional[dict] = None, stream=None) -> dict:
+    """RMS norm of x (+ residual) into MXFP8: dict(codes u8 [M, K], sf, h bf16 [M, K] = x + residual or None).
+
+    weight: bf16 or fp32 [K].  out may hold codes, sf and (with a residual) h;
+    h may be x or the residual itself, which the sum then replaces."""
+    return _rmsnorm_mx("svdq_rmsnorm_mxfp8", x, weight, residual, eps, 1, out, stream)
+
+
+@_on_tensor_device
+def svdq_rmsnorm_mxfp4(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                       eps: float = 1e-6, out: Optional[dict] = None, stream=None) -> dict:
+    """RMS norm of x (+ residual) into MXFP4: dict(codes u8 [M, K/2], sf, h); arguments as svdq_rmsnorm_mxfp8."""
+    return _rmsnorm_mx("svdq_rmsnorm_mxfp4", x, weight, residual, eps, 2, out, stream)
+
+
 def svdq_device_error(stream=None) -> int:
     """Synchronise and return (then clear) the device error word: 0 = nothing
     recorded, 1..6 = a bounded wait ran out, 0x100 + site = a store the debug

@@ -28,8 +28,10 @@
  * svdq_linear -> svdq_score_lambda; svdq_linear_score (the linear with the
  * scoring in its epilogue); svdq_lambda_grid and svdq_bits_lost (lambda
  * candidates and the statistics-only proxy); svdq_quantize_mxfp8 and
- * svdq_linear_mxfp8 (MXFP8 variant); svdq_residual (offline weight
- * conversion); sizes, status strings and svdq_device_error.
+ * svdq_linear_mxfp8 (MXFP8 variant); svdq_quantize_mxfp4 and
+ * svdq_linear_mxfp4 (MXFP4), svdq_dequantize_mxfp8 / _mxfp4 (codes read back) and
+ * svdq_rmsnorm_mxfp8 / _mxfp4 (norm with residual into codes); svdq_residual
+ * (offline weight conversion); sizes, status strings and svdq_device_error.
  *
  * Conventions for every call
  *   - All pointers marked "device" are CUDA device pointers owned by the
@@ -341,6 +343,75 @@ int svdq_linear_mxfp8(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t
                       const void* bias, void* Y, int64_t ldy, int64_t M, int64_t N, int64_t K, void* stream);
 
 /*
+ * MXFP4 (OCP microscaling FP4: E2M1 elements, one E8M0 scale per 32 elements along
+ * K) and norms into the microscaled formats.  No page has a counterpart of these
+ * calls; they take and give the layouts of the MXFP8 variant above, with the codes
+ * packed two a byte as svdq_quantize_act packs them.
+ *
+ * svdq_mxfp4_sf_bytes -- bytes of the scale array of `rows` rows, as
+ * svdq_mxfp8_sf_bytes (0 unless K is a positive multiple of 128).
+ *
+ * svdq_quantize_mxfp4 -- X bf16 [M, K] (device, row stride ldx >= K, ldx * 2 a
+ * multiple of 16, 16-byte aligned) -> codes u8 [M, K/2] (device, row stride K/2,
+ * 16-byte aligned), sf u8 (device, 4-byte aligned, svdq_mxfp4_sf_bytes(M, K)
+ * bytes).  Per 32-element block: e = floor(log2 amax) - 2, at least -127 (-127 for
+ * an all-zero block); scale byte e + 127; code = E2M1(x * 2^-e), nearest even,
+ * magnitudes above 6 saturate, sign kept.  E2M1 has no NaN and no infinity: a block
+ * that holds either gets scale byte 255 (the E8M0 NaN) and zero codes, which makes
+ * every product with it NaN.  Pad rows of the scale layout get 0.  K % 128 == 0
+ * (SVDQ_ERR_UNSUPPORTED otherwise), M >= 1.  X may lie anywhere in a larger buffer;
+ * 32-byte aligned rows are read faster.
+ *
+ * svdq_dequantize_mxfp4, svdq_dequantize_mxfp8 -- the reverse: Y bf16 [M, K] (row
+ * stride ldy >= K, ldy * 2 a multiple of 16, 16-byte aligned) = bf16(dec(code) *
+ * 2^(scale - 127)), the product exact, rounded once; NaN where the scale byte is 255
+ * or the E4M3 code is NaN.  Codes and sf as the quantisers of the format write them
+ * (sf 4-byte aligned).
+ *
+ * svdq_linear_mxfp4 -- Y[m, n] = bf16( sum_k dec(A)[m, k] dec(W)[n, k] + bias[n] ),
+ * dec(v) = E2M1(v) * 2^(scale - 127), fp32 accumulation on the tensor cores (tcgen05
+ * kind::mxf4).  A from svdq_quantize_mxfp4 (or svdq_rmsnorm_mxfp4) of M rows, W from
+ * it on the weight [N, K]; bias bf16 [N] or NULL; Y bf16 [M, N] (device, row stride
+ * ldy >= N, ldy * 2 a multiple of 16, 16-byte aligned; columns past N and rows past M
+ * are left as they were).  K % 128 == 0, N % 8 == 0, 1 <= M <= 2^22.  The order of
+ * the sums depends on (M, N, K) alone: results are bitwise repeatable.
+ *
+ * svdq_rmsnorm_mxfp8, svdq_rmsnorm_mxfp4 -- the residual's addition, the
+ * root-mean-square norm and the quantisation in one pass:
+ *
+ *   h    = bf16(X + residual)                  (h = X when residual is NULL)
+ *   rstd = RN32(1 / sqrt(sum_k h^2 / K + eps))  (squares, sum and root in fp64)
+ *   y    = RN32(RN32(h * rstd) * weight)
+ *   codes, sf = the format's quantisation of y, in fp32 (never rounded to bf16)
+ *
+ * X bf16 [M, K] (row stride ldx); residual bf16 [M, K] (row stride ldr) or NULL; H
+ * bf16 [M, K] (row stride ldh) receives h, NULL exactly when residual is NULL; strides
+ * >= K with stride * 2 a multiple of 16, bases 16-byte aligned.  H may be X's or the
+ * residual's own buffer with the same stride (each element is read before it is
+ * written); it must not overlap them otherwise.  weight: [K], weight_dtype 0 = bf16,
+ * 1 = fp32, 16-byte aligned.  eps > 0, finite.  codes and sf as the quantisers write
+ * them.  A row that holds an infinity or a NaN follows IEEE arithmetic: E4M3 NaN
+ * codes, or NaN block scales in MXFP4.  K % 128 == 0, K <= 32768, M >= 1.
+ *
+ * All are asynchronous on `stream`.
+ */
+size_t svdq_mxfp4_sf_bytes(int64_t rows, int64_t K);
+int svdq_quantize_mxfp4(const void* X, int64_t M, int64_t K, int64_t ldx, uint8_t* codes, uint8_t* sf,
+                        void* stream);
+int svdq_dequantize_mxfp4(const uint8_t* codes, const uint8_t* sf, int64_t M, int64_t K, void* Y, int64_t ldy,
+                          void* stream);
+int svdq_dequantize_mxfp8(const uint8_t* codes, const uint8_t* sf, int64_t M, int64_t K, void* Y, int64_t ldy,
+                          void* stream);
+int svdq_linear_mxfp4(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* w_codes, const uint8_t* w_sf,
+                      const void* bias, void* Y, int64_t ldy, int64_t M, int64_t N, int64_t K, void* stream);
+int svdq_rmsnorm_mxfp8(const void* X, int64_t M, int64_t K, int64_t ldx, const void* residual, int64_t ldr,
+                       const void* weight, int weight_dtype, float eps, void* H, int64_t ldh, uint8_t* codes,
+                       uint8_t* sf, void* stream);
+int svdq_rmsnorm_mxfp4(const void* X, int64_t M, int64_t K, int64_t ldx, const void* residual, int64_t ldr,
+                       const void* weight, int weight_dtype, float eps, void* H, int64_t ldh, uint8_t* codes,
+                       uint8_t* sf, void* stream);
+
+/*
  * svdq_lambda_grid -- lambda candidates over a migration-strength grid
  * ("MiniMax-H3 NVFP4 -- what the smoothing scale should be calibrated on",
  * section "Calibration": the smoothing scale is picked from a grid of
@@ -429,7 +500,8 @@ int svdq_debug_arm_score_timeout(int64_t chunk, int64_t wait_limit_cycles);
  * origin, in 16-byte units of a row x rows), 8 linear fp32 Y, 9 fused scoring
  * partials and results, 10 scoring partials, 11 scoring num / den / rel,
  * 12 residual, 13 lambda grid (lambda, 1/lambda, scales), 14 bits lost,
- * 15 MXFP8 codes, 16 MXFP8 scale bytes.
+ * 15 MX codes, 16 MX scale bytes (quantisers and norms); numbered apart: 32 the
+ * norm's sum of input and residual, 33 read-back values, 34 MXFP4 linear Y.
  *
  * svdq_debug_build -- 1 in the debug library, 0 in the release one.
  *

@@ -549,6 +549,61 @@ def mx_linear(a_codes, a_sf, w_codes, w_sf, bias_bits: Optional[np.ndarray]) -> 
 
 
 # ----------------------------------------------------------------------------
+# MXFP4 and the norms into the microscaled formats (R20, R21)
+# ----------------------------------------------------------------------------
+
+def mx_format_exponent(amax: np.ndarray, emax: int) -> np.ndarray:
+    """floor(log2 amax) - emax, at least -127; -127 where amax is 0 (int64)."""
+    a = np.asarray(amax, np.float64)
+    e = np.frexp(np.where(a > 0, a, 1.0))[1] - 1 - emax
+    return np.where(a > 0, np.maximum(e, -127), -127).astype(np.int64)
+
+
+def mx_quantize_values(y: np.ndarray, fmt: str):
+    """Real values [R, K] -> (codes u8 [R, K], one per element, E8M0 bytes u8 [R, K/32]).
+
+    fmt "mxfp8" (E4M3 bytes) or "mxfp4" (E2M1 codes 0..15).  In mxfp4 a block that
+    holds a NaN or an infinity gets scale byte 255 and zero codes (R20)."""
+    y = np.asarray(y, np.float64)
+    r, k = y.shape
+    if k % MX_BLOCK:
+        raise ValueError("K must be a multiple of 32")
+    b = y.reshape(r, k // MX_BLOCK, MX_BLOCK)
+    bad = ~np.isfinite(b).all(axis=2) if fmt == "mxfp4" else np.zeros(b.shape[:2], bool)
+    b = np.where(bad[:, :, None], 0.0, b)
+    e = mx_format_exponent(np.abs(b).max(axis=2), 2 if fmt == "mxfp4" else 8)
+    q = b * np.exp2(-e.astype(np.float64))[:, :, None]
+    codes = e2m1_encode(q.astype(np.float64)) if fmt == "mxfp4" else e4m3_encode(q)
+    return codes.reshape(r, k).astype(np.uint8), np.where(bad, 255, e + 127).astype(np.uint8)
+
+
+def mx4_dequantize(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """E2M1 codes [R, K] (one per element) and E8M0 bytes [R, K/32] -> fp64 [R, K] (NaN for byte 255)."""
+    r, k = codes.shape
+    s = np.where(scales == 255, np.nan, np.exp2(np.asarray(scales, np.float64) - 127.0))
+    return (e2m1_decode(codes).astype(np.float64).reshape(r, k // MX_BLOCK, MX_BLOCK) * s[:, :, None]).reshape(r, k)
+
+
+def mx4_linear(a_codes, a_sf, w_codes, w_sf, bias_bits: Optional[np.ndarray]) -> np.ndarray:
+    """The MXFP4 linear in fp64: dequant(A) dequant(W)^T + b."""
+    y = mx4_dequantize(a_codes, a_sf) @ mx4_dequantize(w_codes, w_sf).T
+    if bias_bits is not None:
+        y = y + bf16_to_f64(bias_bits)[None, :]
+    return y
+
+
+def rmsnorm(x_bits: np.ndarray, weight: np.ndarray, residual_bits: Optional[np.ndarray], eps: float):
+    """RMS norm (R21): (h bf16 bits, y fp64) with h = bf16(x + residual) or x, y from h in fp64."""
+    h_bits = x_bits
+    if residual_bits is not None:
+        # the exact sum of two bf16 values fits fp64; fp32 addition rounds it once, bf16 a second time
+        h_bits = f32_to_bf16((bf16_to_f32(x_bits) + bf16_to_f32(residual_bits)).astype(np.float32))
+    h = bf16_to_f64(h_bits)
+    rstd = 1.0 / np.sqrt((h * h).mean(axis=1, keepdims=True) + float(np.float32(eps)))
+    return h_bits, h * rstd * np.asarray(weight, np.float64)[None, :]
+
+
+# ----------------------------------------------------------------------------
 # Whole-layer helpers used by the tests
 # ----------------------------------------------------------------------------
 
