@@ -135,9 +135,9 @@ def out_empty(shape, dtype, device):
     """Output buffer of a call: torch.empty, or in debug mode a guarded view
     (plain torch.empty while a CUDA graph is being captured)."""
     import torch
-    if not DEBUG or torch.cuda.is_current_stream_capturing():
-        return torch.empty(shape, dtype=dtype, device=device)
     shape = (shape,) if isinstance(shape, int) else tuple(shape)
+    if not DEBUG or torch.cuda.is_current_stream_capturing():
+        return torch.empty(*shape, dtype=dtype, device=device)   # sizes one by one: parsed faster than a tuple
     n = 1
     for d in shape:
         n *= int(d)

@@ -203,8 +203,10 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
 
 template <int kNT>
 int launch_few(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* w_codes, const uint8_t* w_sf,
-               const Mx4Args& a, cudaStream_t st) {
+               const Mx4Args& args, cudaStream_t st) {
     using L = FewLayout<kNT>;
+    Mx4Args a = args;
+    a.ext_y = debug_extent(kSiteLinearMx4, args.ext_y);
     static std::atomic<uint64_t> smem_set{0};
     auto kern = linear_mx4_few_kernel<kNT>;
     if (!set_dynamic_smem_once(kern, L::kSmem, smem_set)) return SVDQ_ERR_CUDA;
@@ -239,6 +241,294 @@ int launch_few(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* w_cod
     return launch_status(cudaLaunchKernelEx(&cfg, kern, tw, ta, tsw, tsa, a, splits));
 }
 
+// ---------------------------------------------------------------------------
+// Many rows
+// ---------------------------------------------------------------------------
+constexpr int kPairThreads = 384;                // warps: 0 producer, 1 MMA issuer, 4..11 epilogue
+constexpr int kPairEpiWarp0 = 4;
+constexpr int kPairEpiWarps = 8;
+constexpr int kTile = 256;                       // rows and columns of a pair's tile
+
+struct PairLayout {
+    static constexpr int kStages = 5;
+    static constexpr uint32_t kA = 128 * 128, kB = 128 * 128;               // this CTA's half of each
+    static constexpr uint32_t kOffSfa = kA + kB, kOffSfb = kOffSfa + kSfAtoms;
+    static constexpr uint32_t kStage = kOffSfb + 2 * kSfAtoms;              // 35 KB
+    static constexpr uint32_t kOffOut = kStages * kStage;                   // two 32 x 32 bf16 boxes per epilogue warp
+    static constexpr uint32_t kBox = 32 * 64;
+    static constexpr uint32_t kOffBar = kOffOut + kPairEpiWarps * 2 * kBox;
+    static constexpr uint32_t kOffBias = kOffBar + 256;                     // 2 x 256 bf16
+    static constexpr uint32_t kBytes = kOffBias + 2 * kTile * 2;
+    static_assert(kStage % 1024 == 0 && kBytes + 1024 <= 232448, "swizzle atoms aligned; one CTA per SM");
+};
+
+// Tensor memory (512 columns): two accumulators of 256 columns that share 48, and two
+// scale buffers of 24 (A 4 per atom, W 8 per atom, two atoms).  The epilogue reads the
+// shared columns first, so the next tile starts after a quarter of the read-out.
+constexpr uint32_t kPairTmem = 512;
+constexpr uint32_t kAcc1 = 208;
+constexpr uint32_t kPairSf = 464;
+static_assert(kAcc1 + kTile == kPairSf && kPairSf + 48 == kPairTmem, "accumulators and scale buffers fill tensor memory");
+
+struct PairArgs {
+    Mx4Args g;
+    int m_tiles, n_tiles, n_fastest, band;
+    int64_t ext_x, ext_yrow;                     // debug: Y's columns and rows for box origins
+};
+
+// Tile -> (row block, column block).  The smaller operand's blocks are walked fastest, in
+// bands that stay in L2, so the larger one is read once per band.
+__device__ __forceinline__ void pair_tile(const PairArgs& a, int tile, int& m_blk, int& n_blk) {
+    const int fast_tiles = a.n_fastest ? a.n_tiles : a.m_tiles;
+    const int slow_tiles = a.n_fastest ? a.m_tiles : a.n_tiles;
+    const int per_band = a.band * slow_tiles;
+    const int b = tile / per_band, r = tile - b * per_band;
+    const int width = min(a.band, fast_tiles - b * a.band);
+    const int fast = b * a.band + r % width, slow = r / width;
+    m_blk = a.n_fastest ? slow : fast;
+    n_blk = a.n_fastest ? fast : slow;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
+    uint32_t out;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out) : "f"(hi), "f"(lo));
+    return out;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
+                       const __grid_constant__ CUtensorMap tmap_sfa, const __grid_constant__ CUtensorMap tmap_sfw,
+                       const __grid_constant__ CUtensorMap tmap_y, const PairArgs args) {
+    using L = PairLayout;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);        // the first CTA's are used, by both
+    uint64_t* empty = full + L::kStages;
+    uint64_t* acc_full = empty + L::kStages;
+    uint64_t* acc_free = acc_full + 1;                                      // the first CTA's
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 1);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
+    const int tiles = args.m_tiles * args.n_tiles;
+    const int k_stages = args.g.k_stages;
+    uint32_t* err = args.g.err;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_free, 2 * kPairEpiWarps);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, kPairTmem);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();                          // both CTAs' barriers and tensor memory are ready
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_launch_dependents();
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer: this CTA's halves
+        if (lane == 0) {
+            prefetch_tmap(&tmap_a);
+            prefetch_tmap(&tmap_w);
+            prefetch_tmap(&tmap_sfa);
+            prefetch_tmap(&tmap_sfw);
+            pdl_wait();
+            const uint64_t keep = l2_evict_last_policy(), once = l2_evict_first_policy();
+            const uint64_t pol_a = args.n_fastest ? once : keep, pol_w = args.n_fastest ? keep : once;
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs) {
+                int m_blk, n_blk;
+                pair_tile(args, tile, m_blk, n_blk);
+                for (int kb = 0; kb < k_stages; ++kb) {
+                    if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, err, kErrWaitEmpty)) { ok = false; break; }
+                    uint8_t* st = smem + s * L::kStage;
+                    const uint32_t bar = cluster_addr(&full[s], 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::kStage);   // both CTAs' bytes
+                    tma_load_2d_pair(st, &tmap_a, bar, kb * 128, m_blk * kTile + rank * 128, pol_a);
+                    tma_load_2d_pair(st + L::kA, &tmap_w, bar, kb * 128, n_blk * kTile + rank * 128, pol_w);
+                    tma_load_3d_pair(st + L::kOffSfa, &tmap_sfa, bar, 0, kb * 4, m_blk * 2 + rank, pol_a);
+                    tma_load_3d_pair(st + L::kOffSfb, &tmap_sfw, bar, 0, kb * 4, n_blk * 2, pol_w);
+                    if (++s == L::kStages) { s = 0; ph ^= 1u; }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (first CTA)
+        if (rank == 0 && lane == 0) {
+            int s = 0, t = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs, ++t) {
+                if (t > 0 && !mbar_wait(acc_free, (t - 1) & 1, abort_flag, err, kErrWaitAccum)) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + ((t & 1) ? kAcc1 : 0u);
+                for (int kb = 0; kb < k_stages; ++kb) {
+                    if (!mbar_wait(&full[s], ph, abort_flag, err, kErrWaitFull)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t base = smem_u32(smem + s * L::kStage);
+                    const uint64_t da = desc_kmajor_sw128(base), db = desc_kmajor_sw128(base + L::kA);
+                    const uint32_t sfa = tmem + kPairSf + (kb & 1) * 24, sfb = sfa + 8;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        tc_cp_32x128b_x4_pair(sfa + 4 * i, desc_sf_block(base + L::kOffSfa + 512 * i));
+                        tc_cp_32x128b_x4_pair(sfb + 8 * i, desc_sf_block(base + L::kOffSfb + 512 * i));
+                        tc_cp_32x128b_x4_pair(sfb + 8 * i + 4, desc_sf_block(base + L::kOffSfb + kSfAtoms + 512 * i));
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_mxf4_pair(acc, da + 2 * kk, db + 2 * kk, idesc_mxf4(kTile, kTile, 2 * (kk & 1)),
+                                      sfa + 4 * (kk >> 1), sfb + 8 * (kk >> 1), (kb > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit_pair(&empty[s]);
+                    if (++s == L::kStages) { s = 0; ph ^= 1u; }
+                }
+                if (ok) tc_commit_pair(acc_full);
+            }
+        }
+    } else if (warp >= kPairEpiWarp0) {
+        // ------------------------------------------------------------ epilogue: this CTA's 128 rows
+        const int ew = warp - kPairEpiWarp0;
+        const int quarter = warp & 3, half = ew >> 2;        // lane quarter; column half of the tile
+        const int etid = ew * 32 + lane;
+        uint16_t* bias_s = reinterpret_cast<uint16_t*>(smem + L::kOffBias);
+        uint8_t* box = smem + L::kOffOut + ew * 2 * L::kBox;
+        const uint32_t free_bar = cluster_addr(acc_free, 0);
+        const uint64_t pol_y = l2_evict_first_policy();
+        pdl_wait();                                          // bias may come from the kernel before
+        int t = 0;
+        for (int tile = pair; tile < tiles; tile += pairs, ++t) {
+            int m_blk, n_blk;
+            pair_tile(args, tile, m_blk, n_blk);
+            uint16_t* bt = bias_s + (t & 1) * kTile;
+            const int64_t bn = static_cast<int64_t>(n_blk) * kTile + etid;
+            bt[etid] = (args.g.bias && bn < args.g.N) ? args.g.bias[bn] : static_cast<uint16_t>(0);
+            if (bar_sync_or<1, kPairEpiWarps * 32>(*abort_flag != 0u)) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(acc_full, t & 1, abort_flag, err, kErrWaitMma))) continue;
+            tc_fence_after();
+            // Columns shared with the next tile's accumulator: the last 48 of accumulator
+            // 0, the first 48 of accumulator 1.  The warps that hold them read that half of
+            // their columns first and then let the next tile start; the others hold none.
+            const bool owner = half == ((t & 1) ? 0 : 1);
+            if (!owner && lane == 0) mbar_arrive_cluster(free_bar);
+            const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ((t & 1) ? kAcc1 : 0u) + half * 128;
+            const int first = (owner && half == 1) ? 64 : 0;
+            const int32_t row0 = m_blk * kTile + rank * 128 + quarter * 32;
+#pragma unroll 1
+            for (int p = 0; p < 2; ++p) {
+                const int c0 = p == 0 ? first : 64 - first;
+                uint32_t v[2][32];
+                tmem_ld_32x32b_x32(tbase + c0, v[0]);
+                tmem_ld_32x32b_x32(tbase + c0 + 32, v[1]);
+                tmem_ld_wait(v[0]);
+                tmem_ld_tie(v[1]);
+                if (owner && p == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(free_bar);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int col = half * 128 + c0 + 32 * h;
+                    uint8_t* dst = box + h * L::kBox;
+                    if (lane == 0) bulk_wait_read_but_one();         // the box before the last has left its buffer
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t bb = *reinterpret_cast<const uint32_t*>(bt + col + 8 * c + 2 * j);
+                            o[j] = pack_bf16x2_rn(__uint_as_float(v[h][8 * c + 2 * j]) + bf16_lo(bb),
+                                                  __uint_as_float(v[h][8 * c + 2 * j + 1]) + bf16_hi(bb));
+                        }
+                        // 64-byte swizzle: 16-byte piece c of row r sits at c ^ (r / 2 % 4)
+                        *reinterpret_cast<uint4*>(dst + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    fence_async_shared();
+                    __syncwarp();
+                    const int64_t x = static_cast<int64_t>(n_blk) * kTile + col;
+                    if (lane == 0 && row0 < args.g.M && x < args.g.N &&      // boxes wholly past M or N are skipped
+                        box_ok(x, row0, args.ext_x, args.ext_yrow, err, kSiteLinearMx4))
+                        tma_store_2d_hint(&tmap_y, dst, static_cast<int32_t>(x), row0, pol_y);
+                    if (lane == 0) bulk_commit_group();              // an empty group where nothing was stored
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();                          // no remote arrival, copy or MMA of the pair is left
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kPairTmem);
+    }
+}
+
+int launch_pair(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* w_codes, const uint8_t* w_sf,
+                const Mx4Args& g, cudaStream_t st) {
+    using L = PairLayout;
+    static std::atomic<uint64_t> smem_set{0};
+    constexpr uint32_t smem = L::kBytes + 1024;
+    if (!set_dynamic_smem_once(linear_mx4_pair_kernel, smem, smem_set)) return SVDQ_ERR_CUDA;
+    const uint64_t halves = static_cast<uint64_t>(g.K / kMxAtomK) * 2;
+    CUtensorMap ta, tw, tsa, tsw, ty;
+    if (!encode_tmap_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a_codes, g.K / 2, g.M, g.K / 2, 128, 128,
+                        CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w_codes, g.K / 2, g.N, g.K / 2, 128, 128,
+                        CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_3d_u8(&tsa, a_sf, 256, halves, (g.M + 127) / 128, 256, halves * 256, 256, 4, 1) ||
+        !encode_tmap_3d_u8(&tsw, w_sf, 256, halves, (g.N + 127) / 128, 256, halves * 256, 256, 4, 2) ||
+        !encode_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.Y, g.N, g.M, g.ldy * 2, 32, 32,
+                        CU_TENSOR_MAP_SWIZZLE_64B))
+        return SVDQ_ERR_CUDA;
+    PairArgs a = {};
+    a.g = g;
+    a.m_tiles = static_cast<int>((g.M + kTile - 1) / kTile);
+    a.n_tiles = static_cast<int>((g.N + kTile - 1) / kTile);
+    a.n_fastest = g.N <= g.M ? 1 : 0;
+    {
+        // A band of at most 40 MB of the operand walked fastest: each die's half of the L2
+        // holds it beside the other operand's blocks in flight.
+        constexpr int64_t kBandBytes = int64_t(40) << 20;
+        const int64_t fast = a.n_fastest ? a.n_tiles : a.m_tiles;
+        const int64_t bands = (fast * kTile * (g.K / 2) + kBandBytes - 1) / kBandBytes;
+        a.band = static_cast<int>((fast + bands - 1) / bands);
+    }
+    a.ext_x = debug_extent(kSiteLinearMx4, g.N);
+    a.ext_yrow = g.M;
+    const int64_t tiles = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
+    if (tiles > 0x3FFFFFFF) return SVDQ_ERR_UNSUPPORTED;
+    const int64_t sms = device_sm_count() > 1 ? device_sm_count() : 148;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, sms / 2)), 1, 1);
+    cfg.blockDim = dim3(kPairThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return launch_status(cudaLaunchKernelEx(&cfg, linear_mx4_pair_kernel, ta, tw, tsa, tsw, ty, a));
+}
+
 }  // namespace
 }  // namespace svdq
 
@@ -266,11 +556,12 @@ extern "C" int svdq_linear_mxfp4(const uint8_t* a_codes, const uint8_t* a_sf, co
     a.N = N;
     a.K = K;
     a.k_stages = static_cast<int>((K + kStageK - 1) / kStageK);
-    a.ext_y = debug_extent(kSiteLinearMx4, (M - 1) * ldy + N);
+    a.ext_y = (M - 1) * ldy + N;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (M <= 8) return launch_few<8>(a_codes, a_sf, w_codes, w_sf, a, st);
     if (M <= 16) return launch_few<16>(a_codes, a_sf, w_codes, w_sf, a, st);
     if (M <= 32) return launch_few<32>(a_codes, a_sf, w_codes, w_sf, a, st);
     if (M <= 64) return launch_few<64>(a_codes, a_sf, w_codes, w_sf, a, st);
-    return launch_few<128>(a_codes, a_sf, w_codes, w_sf, a, st);
+    if (M <= 128) return launch_few<128>(a_codes, a_sf, w_codes, w_sf, a, st);
+    return launch_pair(a_codes, a_sf, w_codes, w_sf, a, st);
 }

@@ -23,6 +23,9 @@ from . import _lib
 Segs = Optional[Sequence[Tuple[int, int]]]
 
 
+_PLAIN = (bool, int, float, str, torch.dtype)
+
+
 def _tensors_in(v):
     if isinstance(v, torch.Tensor):
         yield v
@@ -42,8 +45,7 @@ def _on_tensor_device(fn):
     params = list(inspect.signature(fn).parameters)
     stream_pos = params.index("stream") if "stream" in params else None
 
-    @functools.wraps(fn)
-    def wrapper(*args, **kwargs):
+    def refuse_or_run(args, kwargs):
         devs = {t.device for a in (*args, *kwargs.values()) for t in _tensors_in(a)}
         if not devs:
             return fn(*args, **kwargs)
@@ -61,6 +63,23 @@ def _on_tensor_device(fn):
         with torch.cuda.device(dev):
             return fn(*args, **kwargs)
 
+    @functools.wraps(fn)
+    def wrapper(*args, **kwargs):
+        # The usual call: every tensor on the current device and no stream given.  Anything
+        # else takes the general path (a few microseconds, as much as a small launch).
+        index = None
+        for a in (*args, *kwargs.values()) if kwargs else args:
+            if isinstance(a, torch.Tensor):
+                i = a.get_device()                       # -1 off the GPU
+                if i < 0 or (index is not None and i != index):
+                    return refuse_or_run(args, kwargs)
+                index = i
+            elif a is not None and not isinstance(a, _PLAIN):
+                return refuse_or_run(args, kwargs)       # a container of tensors, or a stream
+        if index is None or index != torch.cuda.current_device():
+            return refuse_or_run(args, kwargs)
+        return fn(*args, **kwargs)
+
     return wrapper
 
 
@@ -68,9 +87,17 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle by device index, where this torch has the getter
+# (building a Stream object costs about 3 us, as much as a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream: Optional[torch.cuda.Stream]):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check_bf16(t: torch.Tensor, name: str) -> None:
@@ -105,14 +132,15 @@ def _check_matrix(t: Optional[torch.Tensor], dtypes, rows: int, cols: int, name:
     if t is None:
         return
     _check_dense(t, dtypes, 0, name)
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
-    if t.dim() != 2 or t.stride(1) != 1:
+    strides = t.stride()
+    if len(strides) != 2 or strides[1] != 1:
         raise ValueError(f"{name} must be a row-major 2-D tensor")
-    return t.stride(0)
+    return strides[0]
 
 
 def sf_bytes(rows: int, k: int) -> int:
