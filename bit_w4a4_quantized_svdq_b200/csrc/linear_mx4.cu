@@ -244,9 +244,13 @@ int launch_few(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* w_cod
 // ---------------------------------------------------------------------------
 // Many rows
 // ---------------------------------------------------------------------------
-constexpr int kPairThreads = 384;                // warps: 0 producer, 1 MMA issuer, 4..11 epilogue
+constexpr int kPairThreads = 448;                // warps: 0..3 scale writers, 4..11 epilogue, 12 producer, 13 MMA issuer
+constexpr int kPairSfWarps = 4;
 constexpr int kPairEpiWarp0 = 4;
 constexpr int kPairEpiWarps = 8;
+constexpr int kPairLoadWarp = 12;
+constexpr int kPairMmaWarp = 13;
+static_assert(kPairEpiWarp0 % 4 == 0, "each group of four warps covers the four tensor-memory lane quarters (warp % 4)");
 constexpr int kTile = 256;                       // rows and columns of a pair's tile
 
 struct PairLayout {
@@ -262,13 +266,15 @@ struct PairLayout {
     static_assert(kStage % 1024 == 0 && kBytes + 1024 <= 232448, "swizzle atoms aligned; one CTA per SM");
 };
 
-// Tensor memory (512 columns): two accumulators of 256 columns that share 48, and two
-// scale buffers of 24 (A 4 per atom, W 8 per atom, two atoms).  The epilogue reads the
-// shared columns first, so the next tile starts after a quarter of the read-out.
+// Tensor memory (512 columns): two accumulators of 256 columns that share 120, and one
+// scale buffer of 24 columns per ring slot (A 4 per atom, W 8 per atom, two atoms).  The
+// epilogue warps that hold the shared columns read them first and let the next tile
+// start; the other half's warps read theirs meanwhile.
 constexpr uint32_t kPairTmem = 512;
-constexpr uint32_t kAcc1 = 208;
-constexpr uint32_t kPairSf = 464;
-static_assert(kAcc1 + kTile == kPairSf && kPairSf + 48 == kPairTmem, "accumulators and scale buffers fill tensor memory");
+constexpr uint32_t kPairSfCols = 24;
+constexpr uint32_t kPairSf = kPairTmem - PairLayout::kStages * kPairSfCols;
+constexpr uint32_t kAcc1 = kPairSf - kTile;
+static_assert(kAcc1 >= 128, "the shared columns lie in one half of each accumulator");
 
 struct PairArgs {
     Mx4Args g;
@@ -304,7 +310,8 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);        // the first CTA's are used, by both
     uint64_t* empty = full + L::kStages;
-    uint64_t* acc_full = empty + L::kStages;
+    uint64_t* sf_full = empty + L::kStages;                                 // this CTA's scale bytes have landed
+    uint64_t* acc_full = sf_full + L::kStages;
     uint64_t* acc_free = acc_full + 1;                                      // the first CTA's
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
@@ -319,15 +326,16 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::kStages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 1 + 2 * kPairSfWarps);      // operand bytes, and both CTAs' scales in tensor memory
             mbar_init(&empty[s], 1);
+            mbar_init(&sf_full[s], 1);
         }
         mbar_init(acc_full, 1);
         mbar_init(acc_free, 2 * kPairEpiWarps);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == kPairMmaWarp) {
         tmem_alloc_pair(tmem_slot, kPairTmem);
         tmem_relinquish_pair();
     }
@@ -338,7 +346,7 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
     const uint32_t tmem = *tmem_slot;
     pdl_launch_dependents();
 
-    if (warp == 0) {
+    if (warp == kPairLoadWarp) {
         // ------------------------------------------------------------ producer: this CTA's halves
         if (lane == 0) {
             prefetch_tmap(&tmap_a);
@@ -358,18 +366,24 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                     if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, err, kErrWaitEmpty)) { ok = false; break; }
                     uint8_t* st = smem + s * L::kStage;
                     const uint32_t bar = cluster_addr(&full[s], 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::kStage);   // both CTAs' bytes
+                    mbar_arrive_expect_tx(&sf_full[s], 3 * kSfAtoms);
+                    tma_load_3d_hint(st + L::kOffSfa, &tmap_sfa, &sf_full[s], 0, kb * 4, m_blk * 2 + rank, pol_a);
+                    tma_load_3d_hint(st + L::kOffSfb, &tmap_sfw, &sf_full[s], 0, kb * 4, n_blk * 2, pol_w);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (L::kA + L::kB));     // both CTAs' bytes
                     tma_load_2d_pair(st, &tmap_a, bar, kb * 128, m_blk * kTile + rank * 128, pol_a);
                     tma_load_2d_pair(st + L::kA, &tmap_w, bar, kb * 128, n_blk * kTile + rank * 128, pol_w);
-                    tma_load_3d_pair(st + L::kOffSfa, &tmap_sfa, bar, 0, kb * 4, m_blk * 2 + rank, pol_a);
-                    tma_load_3d_pair(st + L::kOffSfb, &tmap_sfw, bar, 0, kb * 4, n_blk * 2, pol_w);
                     if (++s == L::kStages) { s = 0; ph ^= 1u; }
                 }
             }
+            if (!ok) {                                        // a wait ran out: let the copies in flight land (~1 ms)
+                const long long t0 = clock64();
+                while (clock64() - t0 < 2000000) {}
+            }
         }
-    } else if (warp == 1) {
+    } else if (warp == kPairMmaWarp) {
         // ------------------------------------------------------------ MMA issuer (first CTA)
         if (rank == 0 && lane == 0) {
+            const uint64_t da0 = desc_kmajor_sw128(smem_u32(smem)), db0 = desc_kmajor_sw128(smem_u32(smem + L::kA));
             int s = 0, t = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -380,15 +394,8 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                 for (int kb = 0; kb < k_stages; ++kb) {
                     if (!mbar_wait(&full[s], ph, abort_flag, err, kErrWaitFull)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t base = smem_u32(smem + s * L::kStage);
-                    const uint64_t da = desc_kmajor_sw128(base), db = desc_kmajor_sw128(base + L::kA);
-                    const uint32_t sfa = tmem + kPairSf + (kb & 1) * 24, sfb = sfa + 8;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        tc_cp_32x128b_x4_pair(sfa + 4 * i, desc_sf_block(base + L::kOffSfa + 512 * i));
-                        tc_cp_32x128b_x4_pair(sfb + 8 * i, desc_sf_block(base + L::kOffSfb + 512 * i));
-                        tc_cp_32x128b_x4_pair(sfb + 8 * i + 4, desc_sf_block(base + L::kOffSfb + kSfAtoms + 512 * i));
-                    }
+                    const uint64_t da = da0 + s * (L::kStage >> 4), db = db0 + s * (L::kStage >> 4);
+                    const uint32_t sfa = tmem + kPairSf + s * kPairSfCols, sfb = sfa + 8;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_mxf4_pair(acc, da + 2 * kk, db + 2 * kk, idesc_mxf4(kTile, kTile, 2 * (kk & 1)),
@@ -399,7 +406,48 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                 if (ok) tc_commit_pair(acc_full);
             }
         }
-    } else if (warp >= kPairEpiWarp0) {
+    } else if (warp < kPairSfWarps) {
+        // ------------------------------------------------------------ scale writers
+        // One warp per lane quarter copies the stage's scales from shared memory into the
+        // slot's tensor-memory buffer: lane i's four words of an atom are rows i, 32 + i, 64 + i
+        // and 96 + i.  The MMA reads the W scales of all 256 columns in every quarter, and of
+        // the A scales of rows 32 j + i (column j) quarter q only column q.  A slot's scales
+        // land after its last MMAs have completed (the producer waited for them), so the
+        // buffer is free; the shared memory is refilled after the MMAs that wait for the
+        // arrival below, which follows the stores that read these registers.
+        const uint32_t tq = tmem + (static_cast<uint32_t>(warp * 32) << 16) + kPairSf;
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+            for (int kb = 0; kb < k_stages; ++kb) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&sf_full[s], ph, abort_flag, err, kErrWaitFull))) {
+                    ok = false;
+                    break;
+                }
+                const uint8_t* sfa = smem + s * L::kStage + L::kOffSfa;
+                const uint8_t* sfb = smem + s * L::kStage + L::kOffSfb;
+                uint32_t ra[2], rb[16];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    ra[i] = *reinterpret_cast<const uint32_t*>(sfa + i * 512 + lane * 16 + warp * 4);
+                    const uint4 x = *reinterpret_cast<const uint4*>(sfb + i * 512 + lane * 16);
+                    const uint4 y = *reinterpret_cast<const uint4*>(sfb + kSfAtoms + i * 512 + lane * 16);
+                    rb[8 * i] = x.x; rb[8 * i + 1] = x.y; rb[8 * i + 2] = x.z; rb[8 * i + 3] = x.w;
+                    rb[8 * i + 4] = y.x; rb[8 * i + 5] = y.y; rb[8 * i + 6] = y.z; rb[8 * i + 7] = y.w;
+                }
+                const uint32_t base = tq + s * kPairSfCols;
+                tmem_st_32x32b_x1(base + warp, ra[0]);
+                tmem_st_32x32b_x1(base + 4 + warp, ra[1]);
+                tmem_st_32x32b_x16(base + 8, rb);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&full[s], 0));
+                if (++s == L::kStages) { s = 0; ph ^= 1u; }
+            }
+        }
+    } else if (warp < kPairEpiWarp0 + kPairEpiWarps) {
         // ------------------------------------------------------------ epilogue: this CTA's 128 rows
         const int ew = warp - kPairEpiWarp0;
         const int quarter = warp & 3, half = ew >> 2;        // lane quarter; column half of the tile
@@ -419,54 +467,53 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
             if (bar_sync_or<1, kPairEpiWarps * 32>(*abort_flag != 0u)) break;
             if (!__all_sync(0xffffffffu, mbar_wait(acc_full, t & 1, abort_flag, err, kErrWaitMma))) continue;
             tc_fence_after();
-            // Columns shared with the next tile's accumulator: the last 48 of accumulator
-            // 0, the first 48 of accumulator 1.  The warps that hold them read that half of
-            // their columns first and then let the next tile start; the others hold none.
+            // Columns shared with the next tile's accumulator: the last of accumulator 0, the
+            // first of accumulator 1.  The warps of that half let the next tile start once
+            // they have read theirs; the others hold none.
             const bool owner = half == ((t & 1) ? 0 : 1);
             if (!owner && lane == 0) mbar_arrive_cluster(free_bar);
             const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ((t & 1) ? kAcc1 : 0u) + half * 128;
-            const int first = (owner && half == 1) ? 64 : 0;
             const int32_t row0 = m_blk * kTile + rank * 128 + quarter * 32;
-#pragma unroll 1
-            for (int p = 0; p < 2; ++p) {
-                const int c0 = p == 0 ? first : 64 - first;
+            // Two pieces of 32 columns at a time; the first two wait as bf16 while the last are read.
+            uint32_t o[4][16];
+#pragma unroll
+            for (int p = 0; p < 4; p += 2) {
                 uint32_t v[2][32];
-                tmem_ld_32x32b_x32(tbase + c0, v[0]);
-                tmem_ld_32x32b_x32(tbase + c0 + 32, v[1]);
+                tmem_ld_32x32b_x32(tbase + 32 * p, v[0]);
+                tmem_ld_32x32b_x32(tbase + 32 * p + 32, v[1]);
                 tmem_ld_wait(v[0]);
                 tmem_ld_tie(v[1]);
-                if (owner && p == 0) {
+                if (p == 2 && owner) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(free_bar);
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int col = half * 128 + c0 + 32 * h;
-                    uint8_t* dst = box + h * L::kBox;
-                    if (lane == 0) bulk_wait_read_but_one();         // the box before the last has left its buffer
-                    __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t bb = *reinterpret_cast<const uint32_t*>(bt + col + 8 * c + 2 * j);
-                            o[j] = pack_bf16x2_rn(__uint_as_float(v[h][8 * c + 2 * j]) + bf16_lo(bb),
-                                                  __uint_as_float(v[h][8 * c + 2 * j + 1]) + bf16_hi(bb));
-                        }
-                        // 64-byte swizzle: 16-byte piece c of row r sits at c ^ (r / 2 % 4)
-                        *reinterpret_cast<uint4*>(dst + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int j = 0; j < 16; ++j) {
+                        const uint32_t bb = *reinterpret_cast<const uint32_t*>(bt + half * 128 + 32 * (p + h) + 2 * j);
+                        o[p + h][j] = pack_bf16x2_rn(__uint_as_float(v[h][2 * j]) + bf16_lo(bb),
+                                                     __uint_as_float(v[h][2 * j + 1]) + bf16_hi(bb));
                     }
-                    fence_async_shared();
-                    __syncwarp();
-                    const int64_t x = static_cast<int64_t>(n_blk) * kTile + col;
-                    if (lane == 0 && row0 < args.g.M && x < args.g.N &&      // boxes wholly past M or N are skipped
-                        box_ok(x, row0, args.ext_x, args.ext_yrow, err, kSiteLinearMx4))
-                        tma_store_2d_hint(&tmap_y, dst, static_cast<int32_t>(x), row0, pol_y);
-                    if (lane == 0) bulk_commit_group();              // an empty group where nothing was stored
                 }
+            }
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                uint8_t* dst = box + (p & 1) * L::kBox;
+                if (lane == 0) bulk_wait_read_but_one();             // the box before the last has left its buffer
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 4; ++c)                           // 64-byte swizzle: piece c of row r sits at c ^ (r / 2 % 4)
+                    *reinterpret_cast<uint4*>(dst + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+                        make_uint4(o[p][4 * c], o[p][4 * c + 1], o[p][4 * c + 2], o[p][4 * c + 3]);
+                fence_async_shared();
+                __syncwarp();
+                const int64_t x = static_cast<int64_t>(n_blk) * kTile + half * 128 + 32 * p;
+                if (lane == 0 && row0 < args.g.M && x < args.g.N &&          // boxes wholly past M or N are skipped
+                    box_ok(x, row0, args.ext_x, args.ext_yrow, err, kSiteLinearMx4))
+                    tma_store_2d_hint(&tmap_y, dst, static_cast<int32_t>(x), row0, pol_y);
+                if (lane == 0) bulk_commit_group();                  // an empty group where nothing was stored
             }
         }
         if (lane == 0) bulk_wait_all();
@@ -475,7 +522,7 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();                          // no remote arrival, copy or MMA of the pair is left
-    if (warp == 1) {
+    if (warp == kPairMmaWarp) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, kPairTmem);
     }

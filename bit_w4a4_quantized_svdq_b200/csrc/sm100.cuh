@@ -407,10 +407,6 @@ __device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, 
         :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate),
            "r"(sfa_tmem), "r"(sfb_tmem) : "memory");
 }
-// Both CTAs copy from their own shared memory into their own tensor memory.
-__device__ __forceinline__ void tc_cp_32x128b_x4_pair(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(sdesc) : "memory");
-}
 // Arrive on `bar` in both CTAs once every tcgen05 operation this thread issued so far has completed.
 __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
@@ -426,16 +422,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const CUtensorM
         :: "r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar_addr), "l"(policy)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar_addr, int32_t c0,
-                                                 int32_t c1, int32_t c2, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6;"
-        :: "r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar_addr),
-           "l"(policy)
-        : "memory");
-}
-
 // Copy a 32-row x 128-bit shared-memory block into tensor memory, replicated
 // into all four 32-lane quarters (the layout block scales are read from).
 __device__ __forceinline__ void tc_cp_32x128b_x4(uint32_t taddr, uint64_t sdesc) {
@@ -582,7 +568,7 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 
 // Arrive on a barrier of another CTA of the cluster (`addr` from cluster_addr).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
 }
 
 // Full cluster barrier (every thread of every CTA of the cluster).
