@@ -19,6 +19,12 @@ namespace {
 constexpr int kStageK = 256;                     // channels per stage (128 code bytes a row)
 constexpr uint32_t kSfAtoms = 1024;              // scale bytes of 128 rows per stage: two atoms
 
+__device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
+    uint32_t out;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out) : "f"(hi), "f"(lo));
+    return out;
+}
+
 struct Mx4Args {
     const uint16_t* bias;
     uint16_t* Y;
@@ -180,15 +186,46 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
         // in rank order; a wait that ran out has set the error word and still gets here.
         cluster_sync_all();
         if (warp >= 2) {
-            const int row = (warp & 3) * 32 + lane;
-            const int64_t n = static_cast<int64_t>(n_blk) * 128 + row;
-            const float b = (args.bias && n < args.N) ? bf16_lo(args.bias[n]) : 0.0f;
-            for (int t = rank; t < kNT && m0 + t < args.M; t += splits) {
-                float s = 0.0f;
-                for (int r = 0; r < splits; ++r) s += ld_cluster_f32(cluster_addr(smem, r) + (t * 128 + row) * 4);
-                const int64_t off = (m0 + t) * args.ldy + n;
-                if (n < args.N && store_ok(off, 1, args.ext_y, args.err, kSiteLinearMx4))
-                    args.Y[off] = __bfloat16_as_ushort(__float2bfloat16_rn(s + b));
+            // A warp takes activation rows of this rank in turn, a lane four weight rows of one;
+            // kAhead rows' loads are in flight at once (a remote load takes most of a microsecond).
+            constexpr int kAhead = kNT <= 8 ? 1 : 4;
+            const int64_t n = static_cast<int64_t>(n_blk) * 128 + lane * 4;
+            uint2 bb = make_uint2(0u, 0u);
+            if (args.bias && n < args.N) bb = *reinterpret_cast<const uint2*>(args.bias + n);
+            const float b[4] = {bf16_lo(bb.x), bf16_hi(bb.x), bf16_lo(bb.y), bf16_hi(bb.y)};
+            const int rows = min(kNT, static_cast<int>(args.M - m0));
+            for (int t0 = rank + splits * (warp - 2); t0 < rows; t0 += splits * 4 * kAhead) {
+                float4 s[kAhead];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) s[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+                for (int r = 0; r < splits; r += 2) {                // splits is even; added in rank order
+                    float4 p[2][kAhead];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t src = cluster_addr(smem, r + q) + lane * 16;
+#pragma unroll
+                        for (int j = 0; j < kAhead; ++j) {
+                            const int t = t0 + j * splits * 4;
+                            p[q][j] = t < rows ? ld_cluster_f32x4(src + t * 512) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                        for (int j = 0; j < kAhead; ++j) {
+                            s[j].x += p[q][j].x; s[j].y += p[q][j].y; s[j].z += p[q][j].z; s[j].w += p[q][j].w;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    const int t = t0 + j * splits * 4;
+                    const int64_t off = (static_cast<int64_t>(m0) + t) * args.ldy + n;       // N % 8 == 0: four columns or none
+                    if (t < rows && n < args.N && store_ok(off, 4, args.ext_y, args.err, kSiteLinearMx4))
+                        *reinterpret_cast<uint2*>(args.Y + off) =
+                            make_uint2(pack_bf16x2_rn(s[j].x + b[0], s[j].y + b[1]), pack_bf16x2_rn(s[j].z + b[2], s[j].w + b[3]));
+                }
             }
         }
         cluster_sync_all();                      // no CTA leaves while its partials are being read
@@ -258,9 +295,9 @@ struct PairLayout {
     static constexpr uint32_t kA = 128 * 128, kB = 128 * 128;               // this CTA's half of each
     static constexpr uint32_t kOffSfa = kA + kB, kOffSfb = kOffSfa + kSfAtoms;
     static constexpr uint32_t kStage = kOffSfb + 2 * kSfAtoms;              // 35 KB
-    static constexpr uint32_t kOffOut = kStages * kStage;                   // two 32 x 32 bf16 boxes per epilogue warp
-    static constexpr uint32_t kBox = 32 * 64;
-    static constexpr uint32_t kOffBar = kOffOut + kPairEpiWarps * 2 * kBox;
+    static constexpr uint32_t kOffOut = kStages * kStage;                   // one box of 32 rows x 64 bf16 columns per epilogue warp
+    static constexpr uint32_t kBox = 32 * 128;
+    static constexpr uint32_t kOffBar = kOffOut + kPairEpiWarps * kBox;
     static constexpr uint32_t kOffBias = kOffBar + 256;                     // 2 x 256 bf16
     static constexpr uint32_t kBytes = kOffBias + 2 * kTile * 2;
     static_assert(kStage % 1024 == 0 && kBytes + 1024 <= 232448, "swizzle atoms aligned; one CTA per SM");
@@ -268,8 +305,7 @@ struct PairLayout {
 
 // Tensor memory (512 columns): two accumulators of 256 columns that share 120, and one
 // scale buffer of 24 columns per ring slot (A 4 per atom, W 8 per atom, two atoms).  The
-// epilogue warps that hold the shared columns read them first and let the next tile
-// start; the other half's warps read theirs meanwhile.
+// epilogue reads the half that holds the shared columns first and lets the next tile start.
 constexpr uint32_t kPairTmem = 512;
 constexpr uint32_t kPairSfCols = 24;
 constexpr uint32_t kPairSf = kPairTmem - PairLayout::kStages * kPairSfCols;
@@ -293,12 +329,6 @@ __device__ __forceinline__ void pair_tile(const PairArgs& a, int tile, int& m_bl
     const int fast = b * a.band + r % width, slow = r / width;
     m_blk = a.n_fastest ? slow : fast;
     n_blk = a.n_fastest ? fast : slow;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
-    uint32_t out;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out) : "f"(hi), "f"(lo));
-    return out;
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
@@ -450,10 +480,10 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
     } else if (warp < kPairEpiWarp0 + kPairEpiWarps) {
         // ------------------------------------------------------------ epilogue: this CTA's 128 rows
         const int ew = warp - kPairEpiWarp0;
-        const int quarter = warp & 3, half = ew >> 2;        // lane quarter; column half of the tile
+        const int quarter = warp & 3, half = ew >> 2;        // lane quarter; which 64 of each 128 columns
         const int etid = ew * 32 + lane;
         uint16_t* bias_s = reinterpret_cast<uint16_t*>(smem + L::kOffBias);
-        uint8_t* box = smem + L::kOffOut + ew * 2 * L::kBox;
+        uint8_t* box = smem + L::kOffOut + ew * L::kBox;
         const uint32_t free_bar = cluster_addr(acc_free, 0);
         const uint64_t pol_y = l2_evict_first_policy();
         pdl_wait();                                          // bias may come from the kernel before
@@ -467,53 +497,46 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
             if (bar_sync_or<1, kPairEpiWarps * 32>(*abort_flag != 0u)) break;
             if (!__all_sync(0xffffffffu, mbar_wait(acc_full, t & 1, abort_flag, err, kErrWaitMma))) continue;
             tc_fence_after();
-            // Columns shared with the next tile's accumulator: the last of accumulator 0, the
-            // first of accumulator 1.  The warps of that half let the next tile start once
-            // they have read theirs; the others hold none.
-            const bool owner = half == ((t & 1) ? 0 : 1);
-            if (!owner && lane == 0) mbar_arrive_cluster(free_bar);
-            const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ((t & 1) ? kAcc1 : 0u) + half * 128;
+            // The 120 columns shared with the next tile's accumulator lie in the last half of
+            // accumulator 0 and in the first of accumulator 1.  That half is read first, by
+            // all warps (64 columns each), then the next tile may start.
+            const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ((t & 1) ? kAcc1 : 0u);
             const int32_t row0 = m_blk * kTile + rank * 128 + quarter * 32;
-            // Two pieces of 32 columns at a time; the first two wait as bf16 while the last are read.
-            uint32_t o[4][16];
-#pragma unroll
-            for (int p = 0; p < 4; p += 2) {
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+                const int col = (((t & 1) ^ i) ? 0 : 128) + half * 64;
                 uint32_t v[2][32];
-                tmem_ld_32x32b_x32(tbase + 32 * p, v[0]);
-                tmem_ld_32x32b_x32(tbase + 32 * p + 32, v[1]);
+                tmem_ld_32x32b_x32(tbase + col, v[0]);
+                tmem_ld_32x32b_x32(tbase + col + 32, v[1]);
                 tmem_ld_wait(v[0]);
                 tmem_ld_tie(v[1]);
-                if (p == 2 && owner) {
+                if (i == 0) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(free_bar);
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const uint32_t bb = *reinterpret_cast<const uint32_t*>(bt + half * 128 + 32 * (p + h) + 2 * j);
-                        o[p + h][j] = pack_bf16x2_rn(__uint_as_float(v[h][2 * j]) + bf16_lo(bb),
-                                                     __uint_as_float(v[h][2 * j + 1]) + bf16_hi(bb));
-                    }
-                }
-            }
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                uint8_t* dst = box + (p & 1) * L::kBox;
-                if (lane == 0) bulk_wait_read_but_one();             // the box before the last has left its buffer
+                if (lane == 0) bulk_wait_read_all();                 // the previous box has left the buffer
                 __syncwarp();
 #pragma unroll
-                for (int c = 0; c < 4; ++c)                           // 64-byte swizzle: piece c of row r sits at c ^ (r / 2 % 4)
-                    *reinterpret_cast<uint4*>(dst + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
-                        make_uint4(o[p][4 * c], o[p][4 * c + 1], o[p][4 * c + 2], o[p][4 * c + 3]);
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t bb = *reinterpret_cast<const uint32_t*>(bt + col + 8 * c + 2 * j);
+                        const uint32_t* w = v[c >> 2] + 8 * (c & 3) + 2 * j;
+                        o[j] = pack_bf16x2_rn(__uint_as_float(w[0]) + bf16_lo(bb), __uint_as_float(w[1]) + bf16_hi(bb));
+                    }
+                    // 128-byte swizzle: 16-byte piece c of row r sits at c ^ (r % 8)
+                    *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
                 fence_async_shared();
                 __syncwarp();
-                const int64_t x = static_cast<int64_t>(n_blk) * kTile + half * 128 + 32 * p;
+                const int64_t x = static_cast<int64_t>(n_blk) * kTile + col;
                 if (lane == 0 && row0 < args.g.M && x < args.g.N &&          // boxes wholly past M or N are skipped
-                    box_ok(x, row0, args.ext_x, args.ext_yrow, err, kSiteLinearMx4))
-                    tma_store_2d_hint(&tmap_y, dst, static_cast<int32_t>(x), row0, pol_y);
-                if (lane == 0) bulk_commit_group();                  // an empty group where nothing was stored
+                    box_ok(x, row0, args.ext_x, args.ext_yrow, err, kSiteLinearMx4)) {
+                    tma_store_2d_hint(&tmap_y, box, static_cast<int32_t>(x), row0, pol_y);
+                    bulk_commit_group();
+                }
             }
         }
         if (lane == 0) bulk_wait_all();
@@ -542,8 +565,8 @@ int launch_pair(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* w_co
                         CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_tmap_3d_u8(&tsa, a_sf, 256, halves, (g.M + 127) / 128, 256, halves * 256, 256, 4, 1) ||
         !encode_tmap_3d_u8(&tsw, w_sf, 256, halves, (g.N + 127) / 128, 256, halves * 256, 256, 4, 2) ||
-        !encode_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.Y, g.N, g.M, g.ldy * 2, 32, 32,
-                        CU_TENSOR_MAP_SWIZZLE_64B))
+        !encode_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.Y, g.N, g.M, g.ldy * 2, 64, 32,
+                        CU_TENSOR_MAP_SWIZZLE_128B))
         return SVDQ_ERR_CUDA;
     PairArgs a = {};
     a.g = g;

@@ -292,11 +292,6 @@ __device__ __forceinline__ void bulk_wait_read_all() {
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-// As above, but the latest committed store may still be reading.
-__device__ __forceinline__ void bulk_wait_read_but_one() {
-    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
-
 // Wait until every committed bulk store of this thread has completed.
 __device__ __forceinline__ void bulk_wait_all() {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -560,13 +555,17 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
     return a;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
 
-// Arrive on a barrier of another CTA of the cluster (`addr` from cluster_addr).
+// Arrive on a barrier of another CTA of the cluster (`addr` from cluster_addr).  The
+// default scope: what it announces here is tensor memory read or written by completed
+// tcgen05 loads and stores, which no cache holds (a cluster-scope release makes the
+// arriving thread wait for a memory barrier, several hundred cycles a stage).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
 }
