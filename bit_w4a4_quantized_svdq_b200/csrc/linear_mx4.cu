@@ -288,29 +288,33 @@ constexpr int kPairEpiWarps = 8;
 constexpr int kPairLoadWarp = 12;
 constexpr int kPairMmaWarp = 13;
 static_assert(kPairEpiWarp0 % 4 == 0, "each group of four warps covers the four tensor-memory lane quarters (warp % 4)");
-constexpr int kTile = 256;                       // rows and columns of a pair's tile
+constexpr uint32_t kPairTmem = 512;
+constexpr int kTileM = 256;                      // rows of a pair's tile; columns kN: 256 or 128
 
+template <int kN>
 struct PairLayout {
     static constexpr int kStages = 5;
-    static constexpr uint32_t kA = 128 * 128, kB = 128 * 128;               // this CTA's half of each
+    static constexpr int kSfbBlocks = kN == 128 ? 1 : 2;                    // 128-row blocks of W scales a tile touches
+    static constexpr uint32_t kA = 128 * 128, kB = kN / 2 * 128;            // this CTA's half of each
     static constexpr uint32_t kOffSfa = kA + kB, kOffSfb = kOffSfa + kSfAtoms;
-    static constexpr uint32_t kStage = kOffSfb + 2 * kSfAtoms;              // 35 KB
+    static constexpr uint32_t kStage = kOffSfb + kSfbBlocks * kSfAtoms;     // 35 or 26 KB
     static constexpr uint32_t kOffOut = kStages * kStage;                   // one box of 32 rows x 64 bf16 columns per epilogue warp
     static constexpr uint32_t kBox = 32 * 128;
     static constexpr uint32_t kOffBar = kOffOut + kPairEpiWarps * kBox;
     static constexpr uint32_t kOffBias = kOffBar + 256;                     // 2 x 256 bf16
-    static constexpr uint32_t kBytes = kOffBias + 2 * kTile * 2;
+    static constexpr uint32_t kBytes = kOffBias + 2 * 256 * 2;
     static_assert(kStage % 1024 == 0 && kBytes + 1024 <= 232448, "swizzle atoms aligned; one CTA per SM");
+    // Tensor memory (512 columns): two accumulators, then one scale buffer per ring slot (A
+    // 4 columns per atom, W kN / 32 per atom, two atoms).  With 256 columns the accumulators
+    // share 120: the epilogue reads the half that holds them first and lets the next tile start.
+    static constexpr uint32_t kSfCols = 8 + 2 * (kN / 32);
+    static constexpr uint32_t kSf = kPairTmem - kStages * kSfCols;
+    static constexpr bool kShared = kN == 256;
+    static constexpr uint32_t kAcc1 = kShared ? kSf - kN : kN;
+    static_assert(kAcc1 + kN <= kSf && (!kShared || kAcc1 >= 128), "fits; the shared columns lie in one half of each");
+    // more than half an SM's shared memory: never two CTAs waiting for one SM's tensor memory
+    static_assert(kBytes > 116 * 1024, "one CTA per SM");
 };
-
-// Tensor memory (512 columns): two accumulators of 256 columns that share 120, and one
-// scale buffer of 24 columns per ring slot (A 4 per atom, W 8 per atom, two atoms).  The
-// epilogue reads the half that holds the shared columns first and lets the next tile start.
-constexpr uint32_t kPairTmem = 512;
-constexpr uint32_t kPairSfCols = 24;
-constexpr uint32_t kPairSf = kPairTmem - PairLayout::kStages * kPairSfCols;
-constexpr uint32_t kAcc1 = kPairSf - kTile;
-static_assert(kAcc1 >= 128, "the shared columns lie in one half of each accumulator");
 
 struct PairArgs {
     Mx4Args g;
@@ -331,19 +335,20 @@ __device__ __forceinline__ void pair_tile(const PairArgs& a, int tile, int& m_bl
     n_blk = a.n_fastest ? fast : slow;
 }
 
+template <int kN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_w,
                        const __grid_constant__ CUtensorMap tmap_sfa, const __grid_constant__ CUtensorMap tmap_sfw,
                        const __grid_constant__ CUtensorMap tmap_y, const PairArgs args) {
-    using L = PairLayout;
+    using L = PairLayout<kN>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);        // the first CTA's are used, by both
     uint64_t* empty = full + L::kStages;
     uint64_t* sf_full = empty + L::kStages;                                 // this CTA's scale bytes have landed
     uint64_t* acc_full = sf_full + L::kStages;
-    uint64_t* acc_free = acc_full + 1;                                      // the first CTA's
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 1);
+    uint64_t* acc_free = acc_full + 2;                                      // the first CTA's
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 2);
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
     const int warp = threadIdx.x >> 5;
@@ -360,8 +365,10 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
             mbar_init(&empty[s], 1);
             mbar_init(&sf_full[s], 1);
         }
-        mbar_init(acc_full, 1);
-        mbar_init(acc_free, 2 * kPairEpiWarps);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_free[i], 2 * kPairEpiWarps);
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -396,12 +403,12 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                     if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, err, kErrWaitEmpty)) { ok = false; break; }
                     uint8_t* st = smem + s * L::kStage;
                     const uint32_t bar = cluster_addr(&full[s], 0);
-                    mbar_arrive_expect_tx(&sf_full[s], 3 * kSfAtoms);
+                    mbar_arrive_expect_tx(&sf_full[s], (1 + L::kSfbBlocks) * kSfAtoms);
                     tma_load_3d_hint(st + L::kOffSfa, &tmap_sfa, &sf_full[s], 0, kb * 4, m_blk * 2 + rank, pol_a);
-                    tma_load_3d_hint(st + L::kOffSfb, &tmap_sfw, &sf_full[s], 0, kb * 4, n_blk * 2, pol_w);
+                    tma_load_3d_hint(st + L::kOffSfb, &tmap_sfw, &sf_full[s], 0, kb * 4, n_blk * kN / 128, pol_w);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (L::kA + L::kB));     // both CTAs' bytes
-                    tma_load_2d_pair(st, &tmap_a, bar, kb * 128, m_blk * kTile + rank * 128, pol_a);
-                    tma_load_2d_pair(st + L::kA, &tmap_w, bar, kb * 128, n_blk * kTile + rank * 128, pol_w);
+                    tma_load_2d_pair(st, &tmap_a, bar, kb * 128, m_blk * kTileM + rank * 128, pol_a);
+                    tma_load_2d_pair(st + L::kA, &tmap_w, bar, kb * 128, n_blk * kN + rank * (kN / 2), pol_w);
                     if (++s == L::kStages) { s = 0; ph ^= 1u; }
                 }
             }
@@ -418,22 +425,24 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
             uint32_t ph = 0;
             bool ok = true;
             for (int tile = pair; tile < tiles && ok; tile += pairs, ++t) {
-                if (t > 0 && !mbar_wait(acc_free, (t - 1) & 1, abort_flag, err, kErrWaitAccum)) break;
+                // the tile before must have left the shared columns, the one before it this accumulator
+                const int r = t - (L::kShared ? 1 : 2);
+                if (r >= 0 && !mbar_wait(&acc_free[r & 1], (r >> 1) & 1, abort_flag, err, kErrWaitAccum)) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + ((t & 1) ? kAcc1 : 0u);
+                const uint32_t acc = tmem + ((t & 1) ? L::kAcc1 : 0u);
                 for (int kb = 0; kb < k_stages; ++kb) {
                     if (!mbar_wait(&full[s], ph, abort_flag, err, kErrWaitFull)) { ok = false; break; }
                     tc_fence_after();
                     const uint64_t da = da0 + s * (L::kStage >> 4), db = db0 + s * (L::kStage >> 4);
-                    const uint32_t sfa = tmem + kPairSf + s * kPairSfCols, sfb = sfa + 8;
+                    const uint32_t sfa = tmem + L::kSf + s * L::kSfCols, sfb = sfa + 8;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_mxf4_pair(acc, da + 2 * kk, db + 2 * kk, idesc_mxf4(kTile, kTile, 2 * (kk & 1)),
-                                      sfa + 4 * (kk >> 1), sfb + 8 * (kk >> 1), (kb > 0 || kk > 0) ? 1u : 0u);
+                        mma_mxf4_pair(acc, da + 2 * kk, db + 2 * kk, idesc_mxf4(kTileM, kN, 2 * (kk & 1)),
+                                      sfa + 4 * (kk >> 1), sfb + kN / 32 * (kk >> 1), (kb > 0 || kk > 0) ? 1u : 0u);
                     tc_commit_pair(&empty[s]);
                     if (++s == L::kStages) { s = 0; ph ^= 1u; }
                 }
-                if (ok) tc_commit_pair(acc_full);
+                if (ok) tc_commit_pair(&acc_full[t & 1]);
             }
         }
     } else if (warp < kPairSfWarps) {
@@ -445,7 +454,7 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
         // land after its last MMAs have completed (the producer waited for them), so the
         // buffer is free; the shared memory is refilled after the MMAs that wait for the
         // arrival below, which follows the stores that read these registers.
-        const uint32_t tq = tmem + (static_cast<uint32_t>(warp * 32) << 16) + kPairSf;
+        const uint32_t tq = tmem + (static_cast<uint32_t>(warp * 32) << 16) + L::kSf;
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -457,19 +466,21 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                 }
                 const uint8_t* sfa = smem + s * L::kStage + L::kOffSfa;
                 const uint8_t* sfb = smem + s * L::kStage + L::kOffSfb;
-                uint32_t ra[2], rb[16];
+                const uint32_t base = tq + s * L::kSfCols;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    ra[i] = *reinterpret_cast<const uint32_t*>(sfa + i * 512 + lane * 16 + warp * 4);
+                    tmem_st_32x32b_x1(base + 4 * i + warp, *reinterpret_cast<const uint32_t*>(sfa + i * 512 + lane * 16 + warp * 4));
+                    const uint32_t dst = base + 8 + kN / 32 * i;
                     const uint4 x = *reinterpret_cast<const uint4*>(sfb + i * 512 + lane * 16);
-                    const uint4 y = *reinterpret_cast<const uint4*>(sfb + kSfAtoms + i * 512 + lane * 16);
-                    rb[8 * i] = x.x; rb[8 * i + 1] = x.y; rb[8 * i + 2] = x.z; rb[8 * i + 3] = x.w;
-                    rb[8 * i + 4] = y.x; rb[8 * i + 5] = y.y; rb[8 * i + 6] = y.z; rb[8 * i + 7] = y.w;
+                    if constexpr (kN == 128) {
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        tmem_st_32x32b_x4(dst, w);
+                    } else {
+                        const uint4 y = *reinterpret_cast<const uint4*>(sfb + kSfAtoms + i * 512 + lane * 16);
+                        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                        tmem_st_32x32b_x8(dst, w);
+                    }
                 }
-                const uint32_t base = tq + s * kPairSfCols;
-                tmem_st_32x32b_x1(base + warp, ra[0]);
-                tmem_st_32x32b_x1(base + 4 + warp, ra[1]);
-                tmem_st_32x32b_x16(base + 8, rb);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -491,29 +502,30 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
         for (int tile = pair; tile < tiles; tile += pairs, ++t) {
             int m_blk, n_blk;
             pair_tile(args, tile, m_blk, n_blk);
-            uint16_t* bt = bias_s + (t & 1) * kTile;
-            const int64_t bn = static_cast<int64_t>(n_blk) * kTile + etid;
-            bt[etid] = (args.g.bias && bn < args.g.N) ? args.g.bias[bn] : static_cast<uint16_t>(0);
+            uint16_t* bt = bias_s + (t & 1) * 256;
+            const int64_t bn = static_cast<int64_t>(n_blk) * kN + etid;
+            bt[etid] = (args.g.bias && etid < kN && bn < args.g.N) ? args.g.bias[bn] : static_cast<uint16_t>(0);
             if (bar_sync_or<1, kPairEpiWarps * 32>(*abort_flag != 0u)) break;
-            if (!__all_sync(0xffffffffu, mbar_wait(acc_full, t & 1, abort_flag, err, kErrWaitMma))) continue;
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[t & 1], (t >> 1) & 1, abort_flag, err, kErrWaitMma))) continue;
             tc_fence_after();
-            // The 120 columns shared with the next tile's accumulator lie in the last half of
-            // accumulator 0 and in the first of accumulator 1.  That half is read first, by
-            // all warps (64 columns each), then the next tile may start.
-            const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ((t & 1) ? kAcc1 : 0u);
-            const int32_t row0 = m_blk * kTile + rank * 128 + quarter * 32;
+            const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ((t & 1) ? L::kAcc1 : 0u);
+            const int32_t row0 = m_blk * kTileM + rank * 128 + quarter * 32;
+            // 64 columns at a time.  256 columns: the shared ones lie in the last half of
+            // accumulator 0 and in the first of accumulator 1; that half is read first, by
+            // all warps, then the next tile may start.
+            constexpr int pieces = kN / 128;
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
-                const int col = (((t & 1) ^ i) ? 0 : 128) + half * 64;
+            for (int i = 0; i < pieces; ++i) {
+                const int col = (L::kShared ? (((t & 1) ^ i) ? 0 : 128) : 128 * i) + half * 64;
                 uint32_t v[2][32];
                 tmem_ld_32x32b_x32(tbase + col, v[0]);
                 tmem_ld_32x32b_x32(tbase + col + 32, v[1]);
                 tmem_ld_wait(v[0]);
                 tmem_ld_tie(v[1]);
-                if (i == 0) {
+                if (i == (L::kShared ? 0 : pieces - 1)) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(free_bar);
+                    if (lane == 0) mbar_arrive_cluster(free_bar + 8 * (t & 1));
                 }
                 if (lane == 0) bulk_wait_read_all();                 // the previous box has left the buffer
                 __syncwarp();
@@ -531,7 +543,7 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                 }
                 fence_async_shared();
                 __syncwarp();
-                const int64_t x = static_cast<int64_t>(n_blk) * kTile + col;
+                const int64_t x = static_cast<int64_t>(n_blk) * kN + col;
                 if (lane == 0 && row0 < args.g.M && x < args.g.N &&          // boxes wholly past M or N are skipped
                     box_ok(x, row0, args.ext_x, args.ext_yrow, err, kSiteLinearMx4)) {
                     tma_store_2d_hint(&tmap_y, box, static_cast<int32_t>(x), row0, pol_y);
@@ -551,34 +563,35 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
     }
 }
 
+template <int kN>
 int launch_pair(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* w_codes, const uint8_t* w_sf,
                 const Mx4Args& g, cudaStream_t st) {
-    using L = PairLayout;
+    using L = PairLayout<kN>;
     static std::atomic<uint64_t> smem_set{0};
     constexpr uint32_t smem = L::kBytes + 1024;
-    if (!set_dynamic_smem_once(linear_mx4_pair_kernel, smem, smem_set)) return SVDQ_ERR_CUDA;
+    if (!set_dynamic_smem_once(linear_mx4_pair_kernel<kN>, smem, smem_set)) return SVDQ_ERR_CUDA;
     const uint64_t halves = static_cast<uint64_t>(g.K / kMxAtomK) * 2;
     CUtensorMap ta, tw, tsa, tsw, ty;
     if (!encode_tmap_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a_codes, g.K / 2, g.M, g.K / 2, 128, 128,
                         CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w_codes, g.K / 2, g.N, g.K / 2, 128, 128,
+        !encode_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w_codes, g.K / 2, g.N, g.K / 2, 128, kN / 2,
                         CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_tmap_3d_u8(&tsa, a_sf, 256, halves, (g.M + 127) / 128, 256, halves * 256, 256, 4, 1) ||
-        !encode_tmap_3d_u8(&tsw, w_sf, 256, halves, (g.N + 127) / 128, 256, halves * 256, 256, 4, 2) ||
+        !encode_tmap_3d_u8(&tsw, w_sf, 256, halves, (g.N + 127) / 128, 256, halves * 256, 256, 4, L::kSfbBlocks) ||
         !encode_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.Y, g.N, g.M, g.ldy * 2, 64, 32,
                         CU_TENSOR_MAP_SWIZZLE_128B))
         return SVDQ_ERR_CUDA;
     PairArgs a = {};
     a.g = g;
-    a.m_tiles = static_cast<int>((g.M + kTile - 1) / kTile);
-    a.n_tiles = static_cast<int>((g.N + kTile - 1) / kTile);
+    a.m_tiles = static_cast<int>((g.M + kTileM - 1) / kTileM);
+    a.n_tiles = static_cast<int>((g.N + kN - 1) / kN);
     a.n_fastest = g.N <= g.M ? 1 : 0;
     {
         // A band of at most 40 MB of the operand walked fastest: each die's half of the L2
         // holds it beside the other operand's blocks in flight.
         constexpr int64_t kBandBytes = int64_t(40) << 20;
         const int64_t fast = a.n_fastest ? a.n_tiles : a.m_tiles;
-        const int64_t bands = (fast * kTile * (g.K / 2) + kBandBytes - 1) / kBandBytes;
+        const int64_t bands = (fast * (a.n_fastest ? kN : kTileM) * (g.K / 2) + kBandBytes - 1) / kBandBytes;
         a.band = static_cast<int>((fast + bands - 1) / bands);
     }
     a.ext_x = debug_extent(kSiteLinearMx4, g.N);
@@ -596,7 +609,7 @@ int launch_pair(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* w_co
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return launch_status(cudaLaunchKernelEx(&cfg, linear_mx4_pair_kernel, ta, tw, tsa, tsw, ty, a));
+    return launch_status(cudaLaunchKernelEx(&cfg, linear_mx4_pair_kernel<kN>, ta, tw, tsa, tsw, ty, a));
 }
 
 }  // namespace
@@ -633,5 +646,13 @@ extern "C" int svdq_linear_mxfp4(const uint8_t* a_codes, const uint8_t* a_sf, co
     if (M <= 32) return launch_few<32>(a_codes, a_sf, w_codes, w_sf, a, st);
     if (M <= 64) return launch_few<64>(a_codes, a_sf, w_codes, w_sf, a, st);
     if (M <= 128) return launch_few<128>(a_codes, a_sf, w_codes, w_sf, a, st);
-    return launch_pair(a_codes, a_sf, w_codes, w_sf, a, st);
+    // A stage takes about 600 cycles whatever the tile's width (its copies and MMAs share the
+    // SM's memory), so the narrow tile pays only where it costs no further wave: there it has
+    // half the epilogue and twice the pairs at work (256 x 5120 -> 5120: 10.9 against 11.9 us,
+    // 515 x 1920 -> 1160: 6.4 against 8.3; 4096 x 5120 -> 5120: 69 against 43).
+    const int64_t pairs = std::max(device_sm_count() / 2, 1), m_tiles = (M + kTileM - 1) / kTileM;
+    const int64_t waves = (m_tiles * ((N + 255) / 256) + pairs - 1) / pairs;
+    const int64_t waves128 = (m_tiles * ((N + 127) / 128) + pairs - 1) / pairs;
+    if (waves < waves128) return launch_pair<256>(a_codes, a_sf, w_codes, w_sf, a, st);
+    return launch_pair<128>(a_codes, a_sf, w_codes, w_sf, a, st);
 }

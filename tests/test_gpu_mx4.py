@@ -177,7 +177,8 @@ LINEAR_SHAPES = [(1, 128, 128), (1, 8, 256), (1, 5120, 5120), (2, 136, 384), (7,
                  (9, 1160, 1920), (16, 384, 1024), (17, 256, 128), (29, 1280, 5120), (32, 128, 256), (33, 264, 640),
                  (64, 512, 1024), (65, 128, 384), (115, 640, 1280), (128, 256, 512), (129, 392, 640), (255, 512, 256),
                  (256, 256, 128), (257, 520, 1152), (300, 512, 640), (515, 1160, 1920), (1000, 768, 1024),
-                 (1024, 2560, 256), (2050, 136, 512)]
+                 (1024, 2560, 256), (2050, 136, 512), (513, 5000, 256), (512, 5120, 1152), (1800, 2200, 384),
+                 (2304, 2304, 128)]
 
 
 @pytest.mark.parametrize("m,n,k", LINEAR_SHAPES)
@@ -233,6 +234,25 @@ def test_linear_large_sampled(lib):
     a = O.mx4_dequantize(*O.mx_quantize_values(O.bf16_to_f64(L.x[rows]), "mxfp4"))
     w = O.mx4_dequantize(*O.mx_quantize_values(O.bf16_to_f64(L.w), "mxfp4"))
     _check_linear(y[torch.from_numpy(rows).cuda()].contiguous(), a, w, L.bias)
+
+
+# Several tiles per pair of CTAs, 1 to 5 ring slots a tile, and each tile width: 256, 192 and 128 columns.
+@pytest.mark.parametrize("m,n,k", [(4096, 15360, 256), (4000, 15352, 1152), (4096, 5120, 384), (4097, 5112, 128),
+                                   (3000, 9472, 640), (8192, 3712, 256), (2500, 3840, 1408), (16300, 128, 256)])
+def test_linear_many_tiles_sampled(lib, m, n, k):
+    x_bits, w_bits = S.random_bf16((m, k), m, 1.0), S.random_bf16((n, k), n, 0.02)
+    bias = S.random_bf16((n,), 7, 0.05)
+    qa, qw = lib.svdq_quantize_mxfp4(dev_bits(x_bits)), lib.svdq_quantize_mxfp4(dev_bits(w_bits))
+    y = lib.svdq_linear_mxfp4(qa["codes"], qa["sf"], qw["codes"], qw["sf"], dev_bits(bias))
+    rows = np.sort(np.random.default_rng(1).choice(m, 160, replace=False))
+    rows[-1] = m - 1
+    a = O.mx4_dequantize(*O.mx_quantize_values(O.bf16_to_f64(x_bits[rows]), "mxfp4"))
+    w = O.mx4_dequantize(*O.mx_quantize_values(O.bf16_to_f64(w_bits), "mxfp4"))
+    _check_linear(y[torch.from_numpy(rows).cuda()].contiguous(), a, w, bias)
+    for _ in range(5):
+        again = lib.svdq_linear_mxfp4(qa["codes"], qa["sf"], qw["codes"], qw["sf"], dev_bits(bias))
+        assert torch.equal(again.view(torch.int16), y.view(torch.int16))
+    assert lib.svdq_device_error() == 0
 
 
 # ------------------------------------------------------------------------------------------ norms
