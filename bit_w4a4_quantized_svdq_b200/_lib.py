@@ -12,6 +12,8 @@ import ctypes
 import os
 from ctypes import POINTER, Structure, c_char_p, c_float, c_int, c_int64, c_size_t, c_uint32, c_void_p
 
+import torch
+
 from .build import DEBUG_LIB_PATH, LIB_PATH
 
 DEBUG = os.environ.get("SVDQ_DEBUG", "0") not in ("", "0")
@@ -134,7 +136,6 @@ _guarded = []
 def out_empty(shape, dtype, device):
     """Output buffer of a call: torch.empty, or in debug mode a guarded view
     (plain torch.empty while a CUDA graph is being captured)."""
-    import torch
     shape = (shape,) if isinstance(shape, int) else tuple(shape)
     if not DEBUG or torch.cuda.is_current_stream_capturing():
         return torch.empty(*shape, dtype=dtype, device=device)   # sizes one by one: parsed faster than a tuple
@@ -152,7 +153,6 @@ def out_empty(shape, dtype, device):
 def _debug_after(call: str) -> None:
     """After a call in debug mode: wait for it, read (and clear) the device error
     word, and check the guard bands of the outputs allocated since the last call."""
-    import torch
     if torch.cuda.is_current_stream_capturing():
         return
     torch.cuda.synchronize()

@@ -452,7 +452,7 @@ def svdq_linear_mxfp8(a_codes: torch.Tensor, a_sf: torch.Tensor, w_codes: torch.
     _check_dense(bias, _BF16_TYPES, n, "bias", optional=True)
     if out is None:
         out = _lib.out_empty((m, n), torch.bfloat16, a_codes.device)
-    if out.dtype not in _BF16_TYPES or tuple(out.shape) != (m, n):
+    if out.dtype not in _BF16_TYPES or out.shape != (m, n):
         raise ValueError(f"out must be a bf16 [{m}, {n}] tensor")
     _lib.check("svdq_linear_mxfp8", lib.svdq_linear_mxfp8(
         _ptr(a_codes), _ptr(a_sf), _ptr(w_codes), _ptr(w_sf), _ptr(bias), _ptr(out), _row_stride(out, "out"),
@@ -464,9 +464,14 @@ def mxfp4_sf_bytes(rows: int, k: int) -> int:
     return int(_lib.load().svdq_mxfp4_sf_bytes(rows, k))
 
 
+def _mx_sf_size(rows: int, k: int) -> int:
+    """svdq_mxfp8_sf_bytes, here: a call into the library costs more than the arithmetic."""
+    return (rows + 127) // 128 * 128 * (k // 32) if rows >= 1 and k >= 128 and k % 128 == 0 else 0
+
+
 def _mx_outputs(out: Optional[dict], m: int, k: int, code_cols: int, dev) -> dict:
     """Codes [m, code_cols] and scale bytes of a microscaled quantiser: the caller's, checked, or new ones."""
-    nbytes = mxfp8_sf_bytes(m, k)
+    nbytes = _mx_sf_size(m, k)
     if nbytes == 0:
         raise ValueError("K must be a positive multiple of 128 and M at least 1")
     if out is None:
@@ -493,14 +498,14 @@ def _dequantize_mx(name: str, codes: torch.Tensor, sf: torch.Tensor, per_byte: i
     if codes.dim() != 2:
         raise ValueError("codes must be a 2-D byte tensor")
     m, k = codes.shape[0], codes.shape[1] * per_byte
-    nbytes = mxfp8_sf_bytes(m, k)
+    nbytes = _mx_sf_size(m, k)
     if nbytes == 0:
         raise ValueError("K must be a positive multiple of 128 and M at least 1")
     _check_dense(codes, (torch.uint8,), 0, "codes")
     _check_dense(sf, (torch.uint8,), nbytes, "sf")
     if out is None:
         out = _lib.out_empty((m, k), torch.bfloat16, codes.device)
-    if out.dtype not in _BF16_TYPES or tuple(out.shape) != (m, k):
+    if out.dtype not in _BF16_TYPES or out.shape != (m, k):
         raise ValueError(f"out must be a bf16 [{m}, {k}] tensor")
     _lib.check(name, getattr(lib, name)(_ptr(codes), _ptr(sf), m, k, _ptr(out), _row_stride(out, "out"),
                                         _stream(stream)))
@@ -533,12 +538,12 @@ def svdq_linear_mxfp4(a_codes: torch.Tensor, a_sf: torch.Tensor, w_codes: torch.
     n, k = w_codes.shape[0], 2 * kh
     _check_matrix(a_codes, (torch.uint8,), m, kh, "a_codes")
     _check_matrix(w_codes, (torch.uint8,), n, kh, "w_codes")
-    _check_dense(a_sf, (torch.uint8,), mxfp4_sf_bytes(m, k), "a_sf")
-    _check_dense(w_sf, (torch.uint8,), mxfp4_sf_bytes(n, k), "w_sf")
+    _check_dense(a_sf, (torch.uint8,), _mx_sf_size(m, k), "a_sf")
+    _check_dense(w_sf, (torch.uint8,), _mx_sf_size(n, k), "w_sf")
     _check_dense(bias, _BF16_TYPES, n, "bias", optional=True)
     if out is None:
         out = _lib.out_empty((m, n), torch.bfloat16, a_codes.device)
-    if out.dtype not in _BF16_TYPES or tuple(out.shape) != (m, n):
+    if out.dtype not in _BF16_TYPES or out.shape != (m, n):
         raise ValueError(f"out must be a bf16 [{m}, {n}] tensor")
     _lib.check("svdq_linear_mxfp4", lib.svdq_linear_mxfp4(
         _ptr(a_codes), _ptr(a_sf), _ptr(w_codes), _ptr(w_sf), _ptr(bias), _ptr(out), _row_stride(out, "out"),
@@ -555,7 +560,7 @@ def _rmsnorm_mx(name: str, x, weight, residual, eps: float, per_byte: int, out, 
         raise ValueError(f"weight holds {weight.numel()} elements, a row of x {k}")
     if residual is not None:
         _check_bf16(residual, "residual")
-        if tuple(residual.shape) != (m, k):
+        if residual.shape != (m, k):
             raise ValueError(f"residual must be [{m}, {k}], got {list(residual.shape)}")
     h = None if out is None else out.get("h")
     codes = _mx_outputs(out, m, k, k // per_byte, x.device)
@@ -564,7 +569,7 @@ def _rmsnorm_mx(name: str, x, weight, residual, eps: float, per_byte: int, out, 
             raise ValueError("out['h'] is the sum with a residual, and there is none")
     elif h is None:
         h = _lib.out_empty((m, k), torch.bfloat16, x.device)
-    if h is not None and (h.dtype not in _BF16_TYPES or tuple(h.shape) != (m, k)):
+    if h is not None and (h.dtype not in _BF16_TYPES or h.shape != (m, k)):
         raise ValueError(f"out['h'] must be a bf16 [{m}, {k}] tensor")
     _lib.check(name, getattr(lib, name)(
         _ptr(x), m, k, _row_stride(x, "x"), _ptr(residual),

@@ -81,6 +81,9 @@ def test_sizes():
     assert lib.svdq_mxfp4_sf_bytes(1, 128) == 128 * 4
     assert lib.svdq_mxfp4_sf_bytes(129, 5120) == 256 * 160
     assert lib.svdq_mxfp4_sf_bytes(4, 96) == 0 and lib.svdq_mxfp4_sf_bytes(0, 128) == 0
+    for rows in (-1, 0, 1, 127, 128, 129, 5000):
+        for k in (-128, 0, 32, 96, 128, 192, 256, 5120):
+            assert ops._mx_sf_size(rows, k) == ops.mxfp4_sf_bytes(rows, k) == ops.mxfp8_sf_bytes(rows, k)
 
 
 def test_quantize_and_dequantize_reject_bad_arguments():
