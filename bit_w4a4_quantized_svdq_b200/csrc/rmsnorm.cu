@@ -47,20 +47,26 @@ __device__ __forceinline__ float rstd_of(double m) {
     return static_cast<float>(r * (1.5 - 0.5 * m * r * r));
 }
 
+// Two bf16 sums, each rounded once.  (The same bits as an fp32 addition rounded to bf16:
+// where the exponents differ by 16 or less the fp32 sum is exact, and beyond that both
+// give the larger term.)
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
-    float lo, hi;
-    asm("add.rn.f32 %0, %1, %2;" : "=f"(lo) : "f"(bf16_lo(a)), "f"(bf16_lo(b)));
-    asm("add.rn.f32 %0, %1, %2;" : "=f"(hi) : "f"(bf16_hi(a)), "f"(bf16_hi(b)));
     uint32_t o;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(hi), "f"(lo));
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
     return o;
+}
+
+// max(m, |x|), NaN if either is.
+__device__ __forceinline__ float absmax_nan(float m, float x) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(x)));
+    return m;
 }
 
 // kVec: 16-channel pieces per lane (channels 16 t .. of lane t, then 16 (t + T) ..).
 // kSubLanes: lanes of one row where a warp holds several rows (8, 16 or 32), or 0
 // where a row takes the whole CTA.
 template <int kFmt, int kVec, int kSubLanes, bool kW32>
-__global__ void __launch_bounds__(kSubLanes ? 256 : 512, kSubLanes ? 4 : (kVec == 1 ? 2 : 1))
+__global__ void __launch_bounds__(kSubLanes ? 256 : 512, kSubLanes ? 3 : (kVec == 1 ? 2 : 1))
 rmsnorm_mx_kernel(const NormArgs a) {
     constexpr bool kSub = kSubLanes > 0;
     static_assert(!kSub || kVec == 1, "short rows take one piece a lane");
@@ -79,15 +85,25 @@ rmsnorm_mx_kernel(const NormArgs a) {
 
     pdl_launch_dependents();
     pdl_wait();
-    uint32_t wv[kVec][kW32 ? 16 : 8];
+    uint64_t wv[kVec][8];                                                   // the lane's weights as fp32 pairs
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
         const int64_t c = static_cast<int64_t>(t + i * T) * 16;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wv[i][j] = 0ull;
         if (in[i]) {
 #pragma unroll
             for (int j = 0; j < (kW32 ? 4 : 2); ++j) {
                 const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.weight) + c / (kW32 ? 4 : 8) + j);
-                wv[i][4 * j] = w.x; wv[i][4 * j + 1] = w.y; wv[i][4 * j + 2] = w.z; wv[i][4 * j + 3] = w.w;
+                if constexpr (kW32) {
+                    wv[i][2 * j] = pack_f32x2(__uint_as_float(w.x), __uint_as_float(w.y));
+                    wv[i][2 * j + 1] = pack_f32x2(__uint_as_float(w.z), __uint_as_float(w.w));
+                } else {
+                    wv[i][4 * j] = bf16x2_to_f32x2(w.x);
+                    wv[i][4 * j + 1] = bf16x2_to_f32x2(w.y);
+                    wv[i][4 * j + 2] = bf16x2_to_f32x2(w.z);
+                    wv[i][4 * j + 3] = bf16x2_to_f32x2(w.w);
+                }
             }
         }
     }
@@ -150,19 +166,16 @@ rmsnorm_mx_kernel(const NormArgs a) {
         for (int i = 0; i < kVec; ++i) {
             const uint64_t rstd2 = pack_f32x2(rstd, rstd);
             uint64_t y[8];
-            uint32_t m = 0u;
+            float m = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint64_t w2 = !in[i] ? 0ull
-                                    : kW32 ? pack_f32x2(__uint_as_float(wv[i][kW32 ? 2 * j : 0]), __uint_as_float(wv[i][kW32 ? 2 * j + 1 : 0]))
-                                           : bf16x2_to_f32x2(wv[i][j & (kW32 ? 15 : 7)]);
-                y[j] = mul_f32x2(mul_f32x2(bf16x2_to_f32x2(h[i][j]), rstd2), w2);
+                y[j] = mul_f32x2(mul_f32x2(bf16x2_to_f32x2(h[i][j]), rstd2), wv[i][j]);
                 float lo, hi;
                 unpack_f32x2(y[j], lo, hi);
-                m = max(m, max(__float_as_uint(lo) & 0x7FFFFFFFu, __float_as_uint(hi) & 0x7FFFFFFFu));
+                m = absmax_nan(absmax_nan(m, lo), hi);
             }
             uint32_t q[kWords];
-            const uint32_t byte = mx_quantize16<kFmt>(y, m, q);
+            const uint32_t byte = mx_quantize16<kFmt>(y, __float_as_uint(m), q);
             const uint32_t word = mx_scale_word(byte, lane);
             const int64_t c = static_cast<int64_t>(t + i * T) * 16;
             if (!in[i]) continue;
@@ -182,9 +195,9 @@ rmsnorm_mx_kernel(const NormArgs a) {
 template <int kFmt, int kVec, int kSubLanes, bool kW32>
 int norm_launch(const NormArgs& a, int threads, cudaStream_t st) {
     const int rows_per_cta = kSubLanes ? threads / kSubLanes : 1;
-    // resident CTAs: 64 registers a thread allow 1024 threads an SM, 128 allow 512
+    // resident CTAs: 64 registers a thread allow 1024 threads an SM, 80 allow 768, 128 allow 512
     const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 148;
-    const int64_t per_sm = std::max(1, (kVec == 1 ? 1024 : 512) / threads);
+    const int64_t per_sm = std::max(1, (kSubLanes ? 768 : kVec == 1 ? 1024 : 512) / threads);
     const int64_t grid = std::min<int64_t>((a.rows + rows_per_cta - 1) / rows_per_cta, sms * per_sm);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
