@@ -60,6 +60,11 @@ def _on_tensor_device(fn):
             stream = args[stream_pos]
         if stream is not None and stream.device != dev:
             raise ValueError(f"{fn.__name__}: stream is on {stream.device}, tensors on {dev}")
+        if stream is not None:
+            # outputs come from that stream's pool: memory freed after the call is not handed
+            # to another stream while this call's kernels still use it
+            with torch.cuda.stream(stream):
+                return fn(*args, **kwargs)
         with torch.cuda.device(dev):
             return fn(*args, **kwargs)
 

@@ -1,0 +1,26 @@
+"""The MXFP4 and norm tests again, against the debug library, plus its store checks: a
+child pytest with SVDQ_DEBUG=1, as test_gpu_debug_build.py runs the parity suite."""
+import os
+import re
+import subprocess
+import sys
+
+import pytest
+
+from gpu_util import requires_cuda
+
+pytestmark = [pytest.mark.gpu, requires_cuda]
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FILES = ["tests/test_gpu_mx4.py", "tests/gpu_mx4_debug_checks.py"]
+
+
+def test_mx4_suite_and_checks_under_the_debug_library():
+    env = dict(os.environ, SVDQ_DEBUG="1")
+    res = subprocess.run([sys.executable, "-m", "pytest", *FILES, "-m", "gpu", "-x", "-q", "-p", "no:cacheprovider",
+                          "-rs"], cwd=ROOT, env=env, capture_output=True, text=True, timeout=1800)
+    tail = res.stdout[-6000:] + res.stderr[-3000:]
+    assert res.returncode == 0, tail
+    passed = re.search(r"(\d+) passed", res.stdout)
+    assert passed and int(passed.group(1)) >= 100, tail
+    assert "skipped" not in res.stdout.splitlines()[-1], tail
