@@ -76,7 +76,6 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
     const int lane = threadIdx.x & 31;
     const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int n_blk = static_cast<int>(blockIdx.x) / splits;
-    const int m0 = static_cast<int>(blockIdx.y) * kNT;
     const int kb0 = static_cast<int>(static_cast<int64_t>(args.k_stages) * rank / splits);
     const int kb1 = static_cast<int>(static_cast<int64_t>(args.k_stages) * (rank + 1) / splits);
 
@@ -114,8 +113,8 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
                 mbar_arrive_expect_tx(&full[s], L::kStage);
                 tma_load_2d(st, &tmap_w, &full[s], kb * 128, n_blk * 128);
                 tma_load_3d(st + L::kW + L::kA, &tmap_sfw, &full[s], 0, kb * 4, n_blk);
-                tma_load_2d(st + L::kW, &tmap_a, &full[s], kb * 128, m0);
-                tma_load_3d(st + L::kW + L::kA + kSfAtoms, &tmap_sfa, &full[s], 0, kb * 4, m0 / 128);
+                tma_load_2d(st + L::kW, &tmap_a, &full[s], kb * 128, 0);
+                tma_load_3d(st + L::kW + L::kA + kSfAtoms, &tmap_sfa, &full[s], 0, kb * 4, 0);
                 if (++s == L::kStages) { s = 0; ph ^= 1u; }
             }
             // Bounded drain of the copies still in flight (an early exit only).
@@ -170,7 +169,7 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
                 tmem_ld_wait(v);
 #pragma unroll
                 for (int j = 0; j < kC; ++j) {
-                    const int64_t m = m0 + c + j;
+                    const int64_t m = c + j;
                     if (splits > 1) {
                         part[(c + j) * 128 + row] = __uint_as_float(v[j]);
                     } else if (m < args.M && n < args.N && store_ok(m * args.ldy + n, 1, args.ext_y, args.err, kSiteLinearMx4)) {
@@ -193,7 +192,7 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
             uint2 bb = make_uint2(0u, 0u);
             if (args.bias && n < args.N) bb = *reinterpret_cast<const uint2*>(args.bias + n);
             const float b[4] = {bf16_lo(bb.x), bf16_hi(bb.x), bf16_lo(bb.y), bf16_hi(bb.y)};
-            const int rows = min(kNT, static_cast<int>(args.M - m0));
+            const int rows = static_cast<int>(args.M);
             for (int t0 = rank + splits * (warp - 2); t0 < rows; t0 += splits * 4 * kAhead) {
                 float4 s[kAhead];
 #pragma unroll
@@ -221,7 +220,7 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) {
                     const int t = t0 + j * splits * 4;
-                    const int64_t off = (static_cast<int64_t>(m0) + t) * args.ldy + n;       // N % 8 == 0: four columns or none
+                    const int64_t off = t * args.ldy + n;                    // N % 8 == 0: four columns or none
                     if (t < rows && n < args.N && store_ok(off, 4, args.ext_y, args.err, kSiteLinearMx4))
                         *reinterpret_cast<uint2*>(args.Y + off) =
                             make_uint2(pack_bf16x2_rn(s[j].x + b[0], s[j].y + b[1]), pack_bf16x2_rn(s[j].z + b[2], s[j].w + b[3]));
@@ -256,13 +255,13 @@ int launch_few(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* w_cod
         !encode_tmap_3d_u8(&tsw, w_sf, 256, halves, (a.N + 127) / 128, 256, halves * 256, 256, 4, 1) ||
         !encode_tmap_3d_u8(&tsa, a_sf, 256, halves, (a.M + 127) / 128, 256, halves * 256, 256, 4, 1))
         return SVDQ_ERR_CUDA;
-    const int64_t n_blocks = (a.N + 127) / 128, chunks = (a.M + kNT - 1) / kNT;
+    const int64_t n_blocks = (a.N + 127) / 128;
     // Slices of K: as many as keep every CTA resident (two per SM), at most 8 (a portable cluster).
     const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 148;
     int splits = 1;
-    while (splits < 8 && n_blocks * chunks * splits * 2 <= 2 * sms && splits * 2 <= a.k_stages) splits *= 2;
+    while (splits < 8 && n_blocks * splits * 2 <= 2 * sms && splits * 2 <= a.k_stages) splits *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(n_blocks * splits), static_cast<unsigned>(chunks), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(n_blocks * splits), 1, 1);
     cfg.blockDim = dim3(kFewThreads, 1, 1);
     cfg.dynamicSmemBytes = L::kSmem;
     cfg.stream = st;

@@ -40,17 +40,28 @@ __device__ __forceinline__ uint32_t fast_div(const FastDiv& f, uint32_t n) {
     return (__umulhi(f.mul, n) + n) >> f.shift;
 }
 
-// 16 bf16 values (32 bytes) of one lane, read once: one 256-bit access where the
-// address allows it (`wide`, the same for a whole launch), two 128-bit ones otherwise.
-__device__ __forceinline__ void load16_stream(const uint16_t* p, bool wide, uint32_t (&v)[8]) {
+// 16 bf16 values (32 bytes) of one lane: one 256-bit access where the address allows it
+// (`wide`, the same for a whole launch), two 128-bit ones otherwise.
+__device__ __forceinline__ void load16(const uint16_t* p, bool wide, uint32_t (&v)[8]) {
     if (wide) {
-        asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                      : "l"(p) : "memory");
     } else {
         const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 8);
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+}
+
+// The same for values read once: they take no room in L1 and leave L2 first.
+__device__ __forceinline__ void load16_stream(const uint16_t* p, bool wide, uint32_t (&v)[8]) {
+    if (wide) {
+        asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "l"(p) : "memory");
+    } else {
+        load16(p, false, v);
     }
 }
 

@@ -12,9 +12,9 @@
 //
 // Bound by HBM: 2 (x) + 2 (residual) + 2 (h) + 1 + 1/32 (or 1/2 + 1/32) bytes per
 // element.  A lane takes 16 channels (one 256-bit access per tensor), eight lanes an
-// atom; the row stays in registers between the two sums.  CTAs are persistent and walk
-// rows of stride gridDim, the next row's loads issued before the current one is
-// reduced; the weight is read once per CTA.  Rows from M to the layout's 128-row
+// atom; a row of up to 8192 channels stays in registers between the sum and the
+// quantisation.  CTAs are persistent and walk rows of stride gridDim, the next row's
+// loads issued before the current one is reduced; the weight is read once per CTA.  Rows from M to the layout's 128-row
 // padding only write their zero scales.
 #include <algorithm>
 
@@ -62,129 +62,192 @@ __device__ __forceinline__ float absmax_nan(float m, float x) {
     return m;
 }
 
-// kVec: 16-channel pieces per lane (channels 16 t .. of lane t, then 16 (t + T) ..).
-// kSubLanes: lanes of one row where a warp holds several rows (8, 16 or 32), or 0
-// where a row takes the whole CTA.
-template <int kFmt, int kVec, int kSubLanes, bool kW32>
-__global__ void __launch_bounds__(kSubLanes ? 256 : 512, kSubLanes ? 3 : (kVec == 1 ? 2 : 1))
+// Channels 16 t .. 16 t + 15 of the weight as fp32 pairs.
+template <bool kW32>
+__device__ __forceinline__ void load_weight16(const void* weight, int64_t c, uint64_t (&wv)[8]) {
+#pragma unroll
+    for (int j = 0; j < (kW32 ? 4 : 2); ++j) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(weight) + c / (kW32 ? 4 : 8) + j);
+        if constexpr (kW32) {
+            wv[2 * j] = pack_f32x2(__uint_as_float(w.x), __uint_as_float(w.y));
+            wv[2 * j + 1] = pack_f32x2(__uint_as_float(w.z), __uint_as_float(w.w));
+        } else {
+            wv[4 * j] = bf16x2_to_f32x2(w.x);
+            wv[4 * j + 1] = bf16x2_to_f32x2(w.y);
+            wv[4 * j + 2] = bf16x2_to_f32x2(w.z);
+            wv[4 * j + 3] = bf16x2_to_f32x2(w.w);
+        }
+    }
+}
+
+// The sum of the squares of 16 values.
+__device__ __forceinline__ double squares16(const uint32_t (&h)[8], double s) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const double lo = static_cast<double>(bf16_lo(h[j])), hi = static_cast<double>(bf16_hi(h[j]));
+        s = fma(lo, lo, s);
+        s = fma(hi, hi, s);
+    }
+    return s;
+}
+
+// A lane's 16 channels normalised and quantised (every lane of the warp calls this):
+// codes, and the atom's scale word.
+template <int kFmt, int kWords>
+__device__ __forceinline__ uint32_t norm16(const uint32_t (&h)[8], float rstd, const uint64_t (&wv)[8], int lane,
+                                           uint32_t (&q)[kWords]) {
+    const uint64_t rstd2 = pack_f32x2(rstd, rstd);
+    uint64_t y[8];
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        y[j] = mul_f32x2(mul_f32x2(bf16x2_to_f32x2(h[j]), rstd2), wv[j]);
+        float lo, hi;
+        unpack_f32x2(y[j], lo, hi);
+        m = absmax_nan(absmax_nan(m, lo), hi);
+    }
+    return mx_scale_word(mx_quantize16<kFmt>(y, __float_as_uint(m), q), lane);
+}
+
+// The sum of `s` over the CTA's warps, in every thread, in a fixed order.  `part`: one of
+// two buffers used in turn (a row's partials are read before the next row's barrier).
+__device__ __forceinline__ double block_sum(double s, double* part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0.0;
+    const int warps = blockDim.x >> 5;
+    for (int w = 0; w < warps; ++w) s += part[w];
+    return s;
+}
+
+// Rows of up to 8192 channels, held in registers.  kSubLanes: lanes of one row where a
+// warp holds several rows (8, 16 or 32), or 0 where a row takes the whole CTA.
+template <int kFmt, int kSubLanes, bool kW32>
+__global__ void __launch_bounds__(kSubLanes ? 256 : 512, kSubLanes ? 3 : 2)
 rmsnorm_mx_kernel(const NormArgs a) {
     constexpr bool kSub = kSubLanes > 0;
-    static_assert(!kSub || kVec == 1, "short rows take one piece a lane");
     constexpr int kWords = kFmt == kMxFp8 ? 4 : 2;
     __shared__ double part[2][32];
     const int tid = threadIdx.x, lane = tid & 31;
     const int t = kSub ? (tid & (kSubLanes - 1)) : tid;                     // lane within the row
-    const int T = kSub ? kSubLanes : static_cast<int>(blockDim.x);
     const int rows_per_cta = kSub ? static_cast<int>(blockDim.x) / kSubLanes : 1;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * rows_per_cta;
     int64_t row = static_cast<int64_t>(blockIdx.x) * rows_per_cta + (kSub ? tid / kSubLanes : 0);
-    const int64_t atoms = a.K / kMxAtomK;
-    bool in[kVec];
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) in[i] = static_cast<int64_t>(t + i * T) * 16 < a.K;
+    const int64_t c = static_cast<int64_t>(t) * 16;
+    const bool in = c < a.K;
 
     pdl_launch_dependents();
     pdl_wait();
-    uint64_t wv[kVec][8];                                                   // the lane's weights as fp32 pairs
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        const int64_t c = static_cast<int64_t>(t + i * T) * 16;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) wv[i][j] = 0ull;
-        if (in[i]) {
-#pragma unroll
-            for (int j = 0; j < (kW32 ? 4 : 2); ++j) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(a.weight) + c / (kW32 ? 4 : 8) + j);
-                if constexpr (kW32) {
-                    wv[i][2 * j] = pack_f32x2(__uint_as_float(w.x), __uint_as_float(w.y));
-                    wv[i][2 * j + 1] = pack_f32x2(__uint_as_float(w.z), __uint_as_float(w.w));
-                } else {
-                    wv[i][4 * j] = bf16x2_to_f32x2(w.x);
-                    wv[i][4 * j + 1] = bf16x2_to_f32x2(w.y);
-                    wv[i][4 * j + 2] = bf16x2_to_f32x2(w.z);
-                    wv[i][4 * j + 3] = bf16x2_to_f32x2(w.w);
-                }
-            }
-        }
-    }
-    uint32_t nx[kVec][8], nr[kVec][8];                                      // the next row's loads
+    uint64_t wv[8] = {};
+    if (in) load_weight16<kW32>(a.weight, c, wv);
+    uint32_t nx[8], nr[8];                                                  // the next row's loads
     auto fetch = [&](int64_t r) {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const int64_t c = static_cast<int64_t>(t + i * T) * 16;
-            if (in[i] && r < a.M) {
-                load16_stream(a.x + r * a.ldx + c, a.wide_x, nx[i]);
-                if (a.res) load16_stream(a.res + r * a.ldr + c, a.wide_r, nr[i]);
-            }
+        if (in && r < a.M) {
+            load16_stream(a.x + r * a.ldx + c, a.wide_x, nx);
+            if (a.res) load16_stream(a.res + r * a.ldr + c, a.wide_r, nr);
         }
     };
     fetch(row);
     int it = 0;
     // every lane of a warp runs the same number of rounds (the shuffles need them all)
     for (int64_t r0 = row - (kSub ? tid / kSubLanes : 0); r0 < a.rows; r0 += stride, row += stride, ++it) {
-        uint32_t h[kVec][8];
+        uint32_t h[8];
         const bool live = row < a.M;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                h[i][j] = (live && in[i]) ? nx[i][j] : 0u;
-                if (a.res && live && in[i]) h[i][j] = add_bf16x2(h[i][j], nr[i][j]);
-            }
+        for (int j = 0; j < 8; ++j) {
+            h[j] = (live && in) ? nx[j] : 0u;
+            if (a.res && live && in) h[j] = add_bf16x2(h[j], nr[j]);
         }
         fetch(row + stride);
         float rstd = 0.0f;
         // a whole CTA's row past M skips the sums together; a warp's mixed rows run them on zeros
         if (kSub || live) {
-            double s = 0.0;
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const double lo = static_cast<double>(bf16_lo(h[i][j])), hi = static_cast<double>(bf16_hi(h[i][j]));
-                    s = fma(lo, lo, s);
-                    s = fma(hi, hi, s);
-                }
-                if (a.res && live && in[i]) {
-                    const int64_t off = row * a.ldh + static_cast<int64_t>(t + i * T) * 16;
-                    if (store_ok(off, 16, a.ext_h, a.err, kSiteNormH)) store16(a.h + off, a.wide_h, h[i]);
-                }
+            double s = squares16(h, 0.0);
+            if (a.res && live && in) {
+                const int64_t off = row * a.ldh + c;
+                if (store_ok(off, 16, a.ext_h, a.err, kSiteNormH)) store16(a.h + off, a.wide_h, h);
             }
+            if constexpr (kSub) {
 #pragma unroll
-            for (int o = (kSub ? kSubLanes / 2 : 16); o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if constexpr (!kSub) {
-                // two buffers in turn: a row's partials are read before the barrier of the next one's
-                if (lane == 0) part[it & 1][tid >> 5] = s;
-                __syncthreads();
-                s = 0.0;
-                const int warps = T >> 5;
-                for (int w = 0; w < warps; ++w) s += part[it & 1][w];
+                for (int o = kSubLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            } else {
+                s = block_sum(s, part[it & 1]);
             }
             rstd = rstd_of(s * a.inv_k + a.eps);
         }
+        uint32_t q[kWords];
+        const uint32_t word = norm16<kFmt>(h, rstd, wv, lane, q);
+        if (!in) continue;
+        if (live) {
+            const int64_t off = (row * a.K + c) / (kFmt == kMxFp8 ? 1 : 2);
+            if (store_ok(off, 4 * kWords, a.ext_codes, a.err, kSiteMxCodes)) mx_store_codes<kFmt>(a.codes + off, q);
+        }
+        if ((t & 7) == 0 && row < a.rows) {
+            const int64_t off = mx_sf_word(row, c / kMxAtomK, a.K / kMxAtomK);
+            if (store_ok(off, 4, a.ext_sf, a.err, kSiteMxSf))
+                *reinterpret_cast<uint32_t*>(a.sf + off) = live ? word : 0u;
+        }
+    }
+}
+
+// Longer rows, of any length: the first pass forms h and its squares, the second reads h
+// back (each lane its own stores, or x where there is no residual; from L2, the row
+// having just passed) and quantises.
+template <int kFmt, bool kW32>
+__global__ void __launch_bounds__(512, 2)
+rmsnorm_mx_long_kernel(const NormArgs a) {
+    constexpr int kWords = kFmt == kMxFp8 ? 4 : 2;
+    __shared__ double part[2][32];
+    const int lane = threadIdx.x & 31;
+    const int64_t c0 = static_cast<int64_t>(threadIdx.x) * 16;
+    const int64_t step = static_cast<int64_t>(blockDim.x) * 16;
+    const uint16_t* hsrc = a.res ? a.h : a.x;
+    const int64_t ldh = a.res ? a.ldh : a.ldx;
+    const bool wide = a.res ? a.wide_h : a.wide_x;
+    pdl_launch_dependents();
+    pdl_wait();
+    int it = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++it) {
+        const bool live = row < a.M;
+        float rstd = 0.0f;
+        if (live) {
+            double s = 0.0;
+#pragma unroll 2
+            for (int64_t c = c0; c < a.K; c += step) {
+                uint32_t h[8], r[8];
+                load16(a.x + row * a.ldx + c, a.wide_x, h);
+                if (a.res) {
+                    load16_stream(a.res + row * a.ldr + c, a.wide_r, r);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const uint64_t rstd2 = pack_f32x2(rstd, rstd);
-            uint64_t y[8];
-            float m = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                y[j] = mul_f32x2(mul_f32x2(bf16x2_to_f32x2(h[i][j]), rstd2), wv[i][j]);
-                float lo, hi;
-                unpack_f32x2(y[j], lo, hi);
-                m = absmax_nan(absmax_nan(m, lo), hi);
+                    for (int j = 0; j < 8; ++j) h[j] = add_bf16x2(h[j], r[j]);
+                    const int64_t off = row * a.ldh + c;
+                    if (store_ok(off, 16, a.ext_h, a.err, kSiteNormH)) store16(a.h + off, a.wide_h, h);
+                }
+                s = squares16(h, s);
+            }
+            rstd = rstd_of(block_sum(s, part[it & 1]) * a.inv_k + a.eps);
+        }
+        // whole warps take each round: the shuffles need every lane
+#pragma unroll 2
+        for (int64_t c = c0; c - lane * 16 < a.K; c += step) {
+            const bool in = c < a.K;
+            uint32_t h[8] = {};
+            uint64_t wv[8] = {};
+            if (in && live) {
+                load16(hsrc + row * ldh + c, wide, h);
+                load_weight16<kW32>(a.weight, c, wv);
             }
             uint32_t q[kWords];
-            const uint32_t byte = mx_quantize16<kFmt>(y, __float_as_uint(m), q);
-            const uint32_t word = mx_scale_word(byte, lane);
-            const int64_t c = static_cast<int64_t>(t + i * T) * 16;
-            if (!in[i]) continue;
+            const uint32_t word = norm16<kFmt>(h, rstd, wv, lane, q);
+            if (!in) continue;
             if (live) {
                 const int64_t off = (row * a.K + c) / (kFmt == kMxFp8 ? 1 : 2);
                 if (store_ok(off, 4 * kWords, a.ext_codes, a.err, kSiteMxCodes)) mx_store_codes<kFmt>(a.codes + off, q);
             }
-            if ((t & 7) == 0 && row < a.rows) {
-                const int64_t off = mx_sf_word(row, c / kMxAtomK, atoms);
+            if ((lane & 7) == 0) {
+                const int64_t off = mx_sf_word(row, c / kMxAtomK, a.K / kMxAtomK);
                 if (store_ok(off, 4, a.ext_sf, a.err, kSiteMxSf))
                     *reinterpret_cast<uint32_t*>(a.sf + off) = live ? word : 0u;
             }
@@ -192,12 +255,10 @@ rmsnorm_mx_kernel(const NormArgs a) {
     }
 }
 
-template <int kFmt, int kVec, int kSubLanes, bool kW32>
-int norm_launch(const NormArgs& a, int threads, cudaStream_t st) {
-    const int rows_per_cta = kSubLanes ? threads / kSubLanes : 1;
-    // resident CTAs: 64 registers a thread allow 1024 threads an SM, 80 allow 768, 128 allow 512
+// `per_sm`: CTAs resident on an SM (as the kernel's launch bounds allow its registers).
+template <typename Kernel>
+int norm_launch(Kernel kern, const NormArgs& a, int threads, int rows_per_cta, int per_sm, cudaStream_t st) {
     const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 148;
-    const int64_t per_sm = std::max(1, (kSubLanes ? 768 : kVec == 1 ? 1024 : 512) / threads);
     const int64_t grid = std::min<int64_t>((a.rows + rows_per_cta - 1) / rows_per_cta, sms * per_sm);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -208,18 +269,23 @@ int norm_launch(const NormArgs& a, int threads, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return launch_status(cudaLaunchKernelEx(&cfg, rmsnorm_mx_kernel<kFmt, kVec, kSubLanes, kW32>, a));
+    return launch_status(cudaLaunchKernelEx(&cfg, kern, a));
 }
 
 template <int kFmt, bool kW32>
 int norm_dispatch(const NormArgs& a, cudaStream_t st) {
     const int64_t lanes = a.K / 16;
-    if (lanes <= 8) return norm_launch<kFmt, 1, 8, kW32>(a, 256, st);
-    if (lanes <= 16) return norm_launch<kFmt, 1, 16, kW32>(a, 256, st);
-    if (lanes <= 32) return norm_launch<kFmt, 1, 32, kW32>(a, 256, st);
-    if (lanes <= 512) return norm_launch<kFmt, 1, 0, kW32>(a, static_cast<int>((lanes + 31) / 32 * 32), st);
-    if (lanes <= 1024) return norm_launch<kFmt, 2, 0, kW32>(a, static_cast<int>((lanes + 63) / 64 * 32), st);
-    return norm_launch<kFmt, 4, 0, kW32>(a, static_cast<int>((lanes + 127) / 128 * 32), st);
+    if (lanes <= 8) return norm_launch(rmsnorm_mx_kernel<kFmt, 8, kW32>, a, 256, 32, 3, st);
+    if (lanes <= 16) return norm_launch(rmsnorm_mx_kernel<kFmt, 16, kW32>, a, 256, 16, 3, st);
+    if (lanes <= 32) return norm_launch(rmsnorm_mx_kernel<kFmt, 32, kW32>, a, 256, 8, 3, st);
+    if (lanes <= 512) {
+        const int threads = static_cast<int>((lanes + 31) / 32 * 32);
+        return norm_launch(rmsnorm_mx_kernel<kFmt, 0, kW32>, a, threads, 1, 1024 / threads, st);
+    }
+    // as few rounds of at most 512 threads as the row needs, all of them full
+    const int64_t rounds = (lanes + 511) / 512;
+    const int threads = static_cast<int>(((lanes + rounds - 1) / rounds + 31) / 32 * 32);
+    return norm_launch(rmsnorm_mx_long_kernel<kFmt, kW32>, a, threads, 1, 1024 / threads, st);
 }
 
 template <int kFmt>
@@ -230,7 +296,7 @@ int rmsnorm_mx(const void* X, int64_t M, int64_t K, int64_t ldx, const void* res
     if (M < 1 || K < 1 || ldx < K || (residual && (ldr < K || ldh < K))) return SVDQ_ERR_INVALID_ARG;
     if (weight_dtype != 0 && weight_dtype != 1) return SVDQ_ERR_INVALID_ARG;
     if (!(eps > 0.0f) || eps > 3.0e38f) return SVDQ_ERR_INVALID_ARG;
-    if (K % kMxAtomK != 0 || K > 32768 || M > (int64_t(1) << 40)) return SVDQ_ERR_UNSUPPORTED;
+    if (K % kMxAtomK != 0 || K > (int64_t(1) << 30) || M > (int64_t(1) << 40)) return SVDQ_ERR_UNSUPPORTED;
     if (!aligned16(X) || (ldx * 2) % 16 != 0 || !aligned16(weight) || !aligned16(codes) ||
         (reinterpret_cast<uintptr_t>(sf) & 3u))
         return SVDQ_ERR_MISALIGNED;

@@ -560,7 +560,7 @@ def _rmsnorm_mx(name: str, x, weight, residual, eps: float, per_byte: int, out, 
     lib = _lib.load()
     _check_bf16(x, "x")
     m, k = x.shape
-    _check_dense(weight, (torch.bfloat16, torch.float32), 0, "weight")
+    _check_dense(weight, (*_BF16_TYPES, torch.float32), 0, "weight")
     if weight.numel() != k:
         raise ValueError(f"weight holds {weight.numel()} elements, a row of x {k}")
     if residual is not None:

@@ -391,7 +391,7 @@ int svdq_linear_mxfp8(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t
  * written); it must not overlap them otherwise.  weight: [K], weight_dtype 0 = bf16,
  * 1 = fp32, 16-byte aligned.  eps > 0, finite.  codes and sf as the quantisers write
  * them.  A row that holds an infinity or a NaN follows IEEE arithmetic: E4M3 NaN
- * codes, or NaN block scales in MXFP4.  K % 128 == 0, K <= 32768, M >= 1.
+ * codes, or NaN block scales in MXFP4.  K % 128 == 0, M >= 1.
  *
  * All are asynchronous on `stream`.
  */

@@ -280,7 +280,7 @@ def _check_norm(q, x_bits, weight, res_bits, eps, fmt):
 
 
 NORM_SHAPES = [(1, 128), (5, 128), (130, 128), (3, 256), (300, 384), (64, 512), (129, 640), (1, 1920), (1037, 1920),
-               (200, 5120), (1, 8192), (40, 8320), (17, 16384), (9, 20480), (130, 32768)]
+               (200, 5120), (1, 8192), (40, 8320), (17, 16384), (9, 20480), (130, 32768), (3, 40960)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
