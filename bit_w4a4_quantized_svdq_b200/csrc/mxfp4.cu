@@ -13,19 +13,19 @@
 // Both are bound by HBM: 2 bytes of bf16 against 1/2 (or 1) byte of code and 1/32 of
 // scale per element.  Eight lanes take a unit of 128 channels, 16 elements (one
 // 256-bit access) a lane; units are consecutive along the rows, so a warp reads 1 KB
-// contiguous per step and keeps kUnroll of them in flight.  One lane of eight writes
+// contiguous per step and keeps kUnroll of them in flight.  Each warp does that once:
+// with a persistent grid of 8 CTAs an SM the loads and stores of the CTAs ran in step (16384
+// x 20480: quantiser 147 -> 140 us, read-back 146 -> 127 us, which is the copy rate).  One lane of eight writes
 // the unit's four scale bytes as one word.  Rows from M to the layout's 128-row
 // padding get zero scales.
-#include <algorithm>
-
 #include "mx.cuh"
 
 namespace svdq {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
-constexpr int kUnitsPerWarp = 4 * kUnroll;      // per iteration
+constexpr int kThreads = 128;
+constexpr int kUnroll = 3;
+constexpr int kUnitsPerWarp = 4 * kUnroll;
 
 struct MxArgs {
     const uint16_t* x;                          // quantiser input [M, K], row stride ldx
@@ -43,44 +43,41 @@ struct MxArgs {
 __global__ void __launch_bounds__(kThreads)
 mx4_quantize_kernel(const MxArgs a) {
     const int lane = threadIdx.x & 31, sub = lane & 7;
-    const uint32_t warps = gridDim.x * (kThreads / 32);
-    for (uint32_t u0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnitsPerWarp; u0 < a.n_units;
-         u0 += warps * kUnitsPerWarp) {
-        uint32_t v[kUnroll][8];
-        int64_t row[kUnroll];
-        uint32_t atom[kUnroll];
+    const uint32_t u0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnitsPerWarp;
+    uint32_t v[kUnroll][8];
+    int64_t row[kUnroll];
+    uint32_t atom[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const uint32_t u = u0 + 4 * i + (lane >> 3);
-            const uint32_t r = fast_div(a.atoms, u);
-            row[i] = r;
-            atom[i] = u - r * a.atoms.d;
-            if (u < a.n_units && row[i] < a.M) {
-                load16_stream(a.x + row[i] * a.ldx + static_cast<int64_t>(atom[i]) * kMxAtomK + sub * 16, a.wide, v[i]);
-            } else {
+    for (int i = 0; i < kUnroll; ++i) {
+        const uint32_t u = u0 + 4 * i + (lane >> 3);
+        const uint32_t r = fast_div(a.atoms, u);
+        row[i] = r;
+        atom[i] = u - r * a.atoms.d;
+        if (u < a.n_units && row[i] < a.M) {
+            load16_stream(a.x + row[i] * a.ldx + static_cast<int64_t>(atom[i]) * kMxAtomK + sub * 16, a.wide, v[i]);
+        } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = 0u;
-            }
+            for (int j = 0; j < 8; ++j) v[i][j] = 0u;
         }
+    }
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            uint32_t m2 = 0u;                   // |bf16| as bits, two at a time: integer order is value order
-            uint64_t f[8];
+    for (int i = 0; i < kUnroll; ++i) {
+        uint32_t m2 = 0u;                   // |bf16| as bits, two at a time: integer order is value order
+        uint64_t f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                m2 = __vmaxu2(m2, v[i][j] & 0x7FFF7FFFu);
-                f[j] = bf16x2_to_f32x2(v[i][j]);
-            }
-            uint32_t q[2];
-            const uint32_t byte = mx_quantize16<kMxFp4>(f, max(m2 << 16, m2 & 0xFFFF0000u), q);
-            const uint32_t word = mx_scale_word(byte, lane);
-            if (u0 + 4 * i + (lane >> 3) >= a.n_units) continue;
-            const int64_t c = (row[i] * a.K + static_cast<int64_t>(atom[i]) * kMxAtomK) / 2 + sub * 8;
-            if (row[i] < a.M && store_ok(c, 8, a.ext_codes, a.err, kSiteMxCodes)) mx_store_codes<kMxFp4>(a.codes + c, q);
-            const int64_t off = mx_sf_word(row[i], atom[i], a.atoms.d);
-            if (sub == 0 && store_ok(off, 4, a.ext_sf, a.err, kSiteMxSf))
-                *reinterpret_cast<uint32_t*>(a.sf + off) = word;
+        for (int j = 0; j < 8; ++j) {
+            m2 = __vmaxu2(m2, v[i][j] & 0x7FFF7FFFu);
+            f[j] = bf16x2_to_f32x2(v[i][j]);
         }
+        uint32_t q[2];
+        const uint32_t byte = mx_quantize16<kMxFp4>(f, max(m2 << 16, m2 & 0xFFFF0000u), q);
+        const uint32_t word = mx_scale_word(byte, lane);
+        if (u0 + 4 * i + (lane >> 3) >= a.n_units) continue;
+        const int64_t c = (row[i] * a.K + static_cast<int64_t>(atom[i]) * kMxAtomK) / 2 + sub * 8;
+        if (row[i] < a.M && store_ok(c, 8, a.ext_codes, a.err, kSiteMxCodes)) mx_store_codes<kMxFp4>(a.codes + c, q);
+        const int64_t off = mx_sf_word(row[i], atom[i], a.atoms.d);
+        if (sub == 0 && store_ok(off, 4, a.ext_sf, a.err, kSiteMxSf))
+            *reinterpret_cast<uint32_t*>(a.sf + off) = word;
     }
 }
 
@@ -106,44 +103,41 @@ __global__ void __launch_bounds__(kThreads)
 mx_dequantize_kernel(const MxArgs a) {
     constexpr int kWords = kFmt == kMxFp8 ? 4 : 2;          // 16 codes
     const int lane = threadIdx.x & 31, sub = lane & 7;
-    const uint32_t warps = gridDim.x * (kThreads / 32);
-    for (uint32_t u0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnitsPerWarp; u0 < a.n_units;
-         u0 += warps * kUnitsPerWarp) {
-        uint32_t q[kUnroll][kWords], sb[kUnroll];
-        int64_t row[kUnroll], col[kUnroll];
+    const uint32_t u0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnitsPerWarp;
+    uint32_t q[kUnroll][kWords], sb[kUnroll];
+    int64_t row[kUnroll], col[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const uint32_t u = u0 + 4 * i + (lane >> 3);
-            const uint32_t r = fast_div(a.atoms, u), t = u - r * a.atoms.d;
-            row[i] = r;
-            col[i] = static_cast<int64_t>(t) * kMxAtomK + sub * 16;
-            if (u < a.n_units) {
-                sb[i] = __ldg(a.sf + mx_sf_word(row[i], t, a.atoms.d) + (sub >> 1));
-                if constexpr (kFmt == kMxFp8) {
-                    const uint4 w = ldg_stream_v4(a.codes + row[i] * a.K + col[i]);
-                    q[i][0] = w.x; q[i][1] = w.y; q[i][2] = w.z; q[i][3] = w.w;
-                } else {
-                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.codes + (row[i] * a.K + col[i]) / 2));
-                    q[i][0] = w.x; q[i][1] = w.y;
-                }
+    for (int i = 0; i < kUnroll; ++i) {
+        const uint32_t u = u0 + 4 * i + (lane >> 3);
+        const uint32_t r = fast_div(a.atoms, u), t = u - r * a.atoms.d;
+        row[i] = r;
+        col[i] = static_cast<int64_t>(t) * kMxAtomK + sub * 16;
+        if (u < a.n_units) {
+            sb[i] = __ldg(a.sf + mx_sf_word(row[i], t, a.atoms.d) + (sub >> 1));
+            if constexpr (kFmt == kMxFp8) {
+                const uint4 w = ldg_stream_v4(a.codes + row[i] * a.K + col[i]);
+                q[i][0] = w.x; q[i][1] = w.y; q[i][2] = w.z; q[i][3] = w.w;
+            } else {
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.codes + (row[i] * a.K + col[i]) / 2));
+                q[i][0] = w.x; q[i][1] = w.y;
             }
         }
+    }
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            if (u0 + 4 * i + (lane >> 3) >= a.n_units) continue;
-            // 2^(byte - 127): byte 0 is a subnormal fp32, byte 255 is NaN
-            const float s = __uint_as_float(sb[i] == 0u ? 0x00400000u : sb[i] == 255u ? 0x7FC00000u : sb[i] << 23);
-            uint32_t o[8];
+    for (int i = 0; i < kUnroll; ++i) {
+        if (u0 + 4 * i + (lane >> 3) >= a.n_units) continue;
+        // 2^(byte - 127): byte 0 is a subnormal fp32, byte 255 is NaN
+        const float s = __uint_as_float(sb[i] == 0u ? 0x00400000u : sb[i] == 255u ? 0x7FC00000u : sb[i] << 23);
+        uint32_t o[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t h = kFmt == kMxFp8 ? e4m3x2_to_f16x2(q[i][j >> 1] >> (16 * (j & 1)))
-                                                  : e2m1x2_to_f16x2((q[i][j >> 2] >> (8 * (j & 3))) & 0xFFu);
-                const float lo = __fmul_rn(f16_bits_to_f32(h), s), hi = __fmul_rn(f16_bits_to_f32(h >> 16), s);
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(hi), "f"(lo));
-            }
-            const int64_t off = row[i] * a.ldx + col[i];
-            if (store_ok(off, 16, a.ext_y, a.err, kSiteMxValues)) store16(a.y + off, a.wide, o);
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t h = kFmt == kMxFp8 ? e4m3x2_to_f16x2(q[i][j >> 1] >> (16 * (j & 1)))
+                                              : e2m1x2_to_f16x2((q[i][j >> 2] >> (8 * (j & 3))) & 0xFFu);
+            const float lo = __fmul_rn(f16_bits_to_f32(h), s), hi = __fmul_rn(f16_bits_to_f32(h >> 16), s);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(hi), "f"(lo));
         }
+        const int64_t off = row[i] * a.ldx + col[i];
+        if (store_ok(off, 16, a.ext_y, a.err, kSiteMxValues)) store16(a.y + off, a.wide, o);
     }
 }
 
@@ -176,9 +170,8 @@ int mx_prepare(const void* v, int64_t M, int64_t K, int64_t ldx, const uint8_t* 
 }
 
 unsigned mx_grid(uint32_t units) {
-    const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 148;
-    const int64_t per_block = (kThreads / 32) * kUnitsPerWarp;
-    return static_cast<unsigned>(std::min<int64_t>((units + per_block - 1) / per_block, sms * 8));
+    constexpr uint32_t per_block = (kThreads / 32) * kUnitsPerWarp;
+    return (units + per_block - 1) / per_block;
 }
 
 template <int kFmt>
