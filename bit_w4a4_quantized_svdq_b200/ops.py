@@ -113,6 +113,7 @@ def _check_bf16(t: torch.Tensor, name: str) -> None:
 
 
 _BF16_TYPES = (torch.bfloat16, torch.int16, torch.uint16)
+_U8 = (torch.uint8,)
 
 
 def _check_dense(t: Optional[torch.Tensor], dtypes, min_numel: int, name: str, optional: bool = False) -> None:
@@ -123,6 +124,8 @@ def _check_dense(t: Optional[torch.Tensor], dtypes, min_numel: int, name: str, o
         if optional:
             return
         raise ValueError(f"{name} is required")
+    if t.dtype in dtypes and t.is_contiguous() and t.numel() >= min_numel:
+        return
     if t.dtype not in dtypes:
         want = " or ".join(str(d) for d in dtypes)
         raise TypeError(f"{name} must be {want}, got {t.dtype}")
@@ -134,7 +137,7 @@ def _check_dense(t: Optional[torch.Tensor], dtypes, min_numel: int, name: str, o
 
 def _check_matrix(t: Optional[torch.Tensor], dtypes, rows: int, cols: int, name: str) -> None:
     """A contiguous [rows, cols] tensor of one of `dtypes` (None passes)."""
-    if t is None:
+    if t is None or (t.dtype in dtypes and t.shape == (rows, cols) and t.is_contiguous()):
         return
     _check_dense(t, dtypes, 0, name)
     if t.shape != (rows, cols):
@@ -480,7 +483,7 @@ def _mx_outputs(out: Optional[dict], m: int, k: int, code_cols: int, dev) -> dic
     if nbytes == 0:
         raise ValueError("K must be a positive multiple of 128 and M at least 1")
     if out is None:
-        out = dict(codes=_lib.out_empty((m, code_cols), torch.uint8, dev), sf=_lib.out_empty(nbytes, torch.uint8, dev))
+        return dict(codes=_lib.out_empty((m, code_cols), torch.uint8, dev), sf=_lib.out_empty((nbytes,), torch.uint8, dev))
     _check_dense(out["codes"], (torch.uint8,), m * code_cols, "out['codes']")
     _check_dense(out["sf"], (torch.uint8,), nbytes, "out['sf']")
     return out
@@ -541,14 +544,14 @@ def svdq_linear_mxfp4(a_codes: torch.Tensor, a_sf: torch.Tensor, w_codes: torch.
         raise ValueError("a_codes and w_codes must be 2-D [rows, K/2] byte tensors")
     m, kh = a_codes.shape
     n, k = w_codes.shape[0], 2 * kh
-    _check_matrix(a_codes, (torch.uint8,), m, kh, "a_codes")
-    _check_matrix(w_codes, (torch.uint8,), n, kh, "w_codes")
-    _check_dense(a_sf, (torch.uint8,), _mx_sf_size(m, k), "a_sf")
-    _check_dense(w_sf, (torch.uint8,), _mx_sf_size(n, k), "w_sf")
+    _check_dense(a_codes, _U8, 0, "a_codes")
+    _check_matrix(w_codes, _U8, n, kh, "w_codes")
+    _check_dense(a_sf, _U8, _mx_sf_size(m, k), "a_sf")
+    _check_dense(w_sf, _U8, _mx_sf_size(n, k), "w_sf")
     _check_dense(bias, _BF16_TYPES, n, "bias", optional=True)
     if out is None:
         out = _lib.out_empty((m, n), torch.bfloat16, a_codes.device)
-    if out.dtype not in _BF16_TYPES or out.shape != (m, n):
+    elif out.dtype not in _BF16_TYPES or out.shape != (m, n):
         raise ValueError(f"out must be a bf16 [{m}, {n}] tensor")
     _lib.check("svdq_linear_mxfp4", lib.svdq_linear_mxfp4(
         _ptr(a_codes), _ptr(a_sf), _ptr(w_codes), _ptr(w_sf), _ptr(bias), _ptr(out), _row_stride(out, "out"),
