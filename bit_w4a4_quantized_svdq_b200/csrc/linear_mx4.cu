@@ -3,12 +3,29 @@
 //
 //   Y[m, n] = bf16( sum_k dec(A)[m, k] dec(W)[n, k] + bias[n] ),  fp32 accumulation
 //
-// few rows: the weight is what has to be read, (K/2 + K/32) bytes a row of W.  The
-// MMA takes 128 rows of W as its M operand and the activation rows (8 to 128) as its N
-// operand, so no tensor-core row is spent on rows that are not there.  A CTA owns one
-// block of 128 weight rows and a slice of K; the slices of one block are a cluster,
-// whose partial sums meet over distributed shared memory in rank order (no workspace,
-// no atomics: bitwise repeatable).
+// Up to 128 rows (linear_mx4_few_kernel): the weight is what has to be read, K/2 + K/32
+// bytes a row of W.  The MMA takes 128 rows of W as its M operand and the activation rows
+// (8 to 128) as its N operand, so no tensor-core row is spent on rows that are not there.
+// A CTA owns one block of 128 weight rows and a slice of K; the slices of one block are a
+// cluster, whose partial sums meet over distributed shared memory in rank order (no
+// workspace, no atomics: bitwise repeatable).  One row, 5120 -> 5120: 5.3 us (14 MB; 2.1 us
+// at the copy rate, and 3.7 us is what the smallest such call takes: launch, set-up, two
+// cluster barriers); 29 rows, 5120 -> 15360: 8.8 us, 4.9 TB/s.
+//
+// More rows (linear_mx4_pair_kernel): persistent pairs of CTAs walk 256 x 256 tiles
+// (256 x 128 where that costs no further wave) with cta_group::2 MMAs, each CTA loading half
+// of A's and half of W's rows: 32 KB of codes a 256-channel stage and SM, where one CTA of
+// 128 x 256 loads 48.  One thread loads, one issues the MMAs, four warps per CTA move block
+// scales into tensor memory, eight read the accumulator out.
+//   16384 x 20480 -> 5120  570-600 us (6.0-5.7 PFLOP/s), 650 in a loop that runs into the power limit
+//   4096 x 5120 -> 15360   117-120 us (5.5-5.4), 4096 x 5120 -> 5120  43 us (5.0; 4.3 waves of tiles)
+// What paces a stage of 256 x 256 x 256, in SM cycles: its MMAs alone 526, its copies alone
+// 448, both 588, with the scales 606 (a tile 128 columns wide: 355, 402, 572, 593; neither the
+// number of copies nor a deeper ring changes that); 800 more at a tile's end, of which the
+// wait for the shared accumulator columns is 620.
+// The scales do not go by tcgen05.cp: a copy holds the MMA behind it up by about 45 cycles,
+// six a stage (805 us on the first shape), and between the MMAs or a stage ahead it is no
+// better (876, 838).
 #include <algorithm>
 
 #include "mx.cuh"
@@ -72,8 +89,7 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
-    const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int n_blk = static_cast<int>(blockIdx.x) / splits;
     const int kb0 = static_cast<int>(static_cast<int64_t>(args.k_stages) * rank / splits);
@@ -117,7 +133,7 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
                 tma_load_3d(st + L::kW + L::kA + kSfAtoms, &tmap_sfa, &full[s], 0, kb * 4, 0);
                 if (++s == L::kStages) { s = 0; ph ^= 1u; }
             }
-            // Bounded drain of the copies still in flight (an early exit only).
+            // Bounded drain: a copy may still be in flight where a wait ran out.
             for (int i = (it > L::kStages ? it - L::kStages : 0); i < it; ++i) {
                 const long long t0 = clock64();
                 while (!mbar_try_wait(&full[i % L::kStages], (i / L::kStages) & 1) && clock64() - t0 < kWaitLimitCycles) {}
@@ -256,7 +272,8 @@ int launch_few(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* w_cod
         !encode_tmap_3d_u8(&tsa, a_sf, 256, halves, (a.M + 127) / 128, 256, halves * 256, 256, 4, 1))
         return SVDQ_ERR_CUDA;
     const int64_t n_blocks = (a.N + 127) / 128;
-    // Slices of K: as many as keep every CTA resident (two per SM), at most 8 (a portable cluster).
+    // Slices of K: as many as keep every CTA resident (two per SM), at most 8 (a portable
+    // cluster).  One row, 5120 -> 5120: 4 slices 5.3 us; 2 slices 6.9, 8 slices (two waves) 9.3.
     const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 148;
     int splits = 1;
     while (splits < 8 && n_blocks * splits * 2 <= 2 * sms && splits * 2 <= a.k_stages) splits *= 2;
@@ -640,15 +657,17 @@ extern "C" int svdq_linear_mxfp4(const uint8_t* a_codes, const uint8_t* a_sf, co
     a.k_stages = static_cast<int>((K + kStageK - 1) / kStageK);
     a.ext_y = (M - 1) * ldy + N;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // Up to 128 rows the tile's N operand is the rows themselves (128 rows, 5120 -> 5120: 10.9 us;
+    // 129 rows in a pair's 256-row tiles 10.2, and one row there would take as long).
     if (M <= 8) return launch_few<8>(a_codes, a_sf, w_codes, w_sf, a, st);
     if (M <= 16) return launch_few<16>(a_codes, a_sf, w_codes, w_sf, a, st);
     if (M <= 32) return launch_few<32>(a_codes, a_sf, w_codes, w_sf, a, st);
     if (M <= 64) return launch_few<64>(a_codes, a_sf, w_codes, w_sf, a, st);
     if (M <= 128) return launch_few<128>(a_codes, a_sf, w_codes, w_sf, a, st);
-    // A stage takes about 600 cycles whatever the tile's width (its copies and MMAs share the
-    // SM's memory), so the narrow tile pays only where it costs no further wave: there it has
-    // half the epilogue and twice the pairs at work (256 x 5120 -> 5120: 10.9 against 11.9 us,
-    // 515 x 1920 -> 1160: 6.4 against 8.3; 4096 x 5120 -> 5120: 69 against 43).
+    // A stage takes about 600 cycles whatever the tile's width, so the narrow tile pays only
+    // where it costs no further wave: there it has half the epilogue and twice the pairs at
+    // work (256 x 5120 -> 5120: 10.4 against 11.9 us, 515 x 1920 -> 1160: 6.2 against 8.3;
+    // 4096 x 5120 -> 5120: 69 against 43).
     const int64_t pairs = std::max(device_sm_count() / 2, 1), m_tiles = (M + kTileM - 1) / kTileM;
     const int64_t waves = (m_tiles * ((N + 255) / 256) + pairs - 1) / pairs;
     const int64_t waves128 = (m_tiles * ((N + 127) / 128) + pairs - 1) / pairs;

@@ -8,14 +8,17 @@
 //
 // The sum is held in fp64 because the codes are decided by comparing y with rounding
 // borders: with it rstd is the correctly rounded value in all but about one row in
-// 2^20, so equal inputs give equal codes whatever the launch shape.
+// 2^18, so equal inputs give equal codes whatever the launch shape.
 //
 // Bound by HBM: 2 (x) + 2 (residual) + 2 (h) + 1 + 1/32 (or 1/2 + 1/32) bytes per
 // element.  A lane takes 16 channels (one 256-bit access per tensor), eight lanes an
 // atom; a row of up to 8192 channels stays in registers between the sum and the
 // quantisation.  A CTA walks rows of stride gridDim, the next row's loads issued before
-// the current one is reduced; the weight is read once per CTA.  Rows from M to the layout's 128-row
-// padding only write their zero scales.
+// the current one is reduced; the weight is read once per CTA.  Rows from M to the
+// layout's 128-row padding only write their zero scales.
+//   16384 x 5120 with residual: into MXFP8 95-97 us (6.1 TB/s; a plain copy 6.5), into
+//   MXFP4 92; 4096 x 5120 27 us; one row 2.5 us; 16384 x 20480 (two passes) 453-477 us.
+//   Without the next row's loads ahead 16384 x 5120 takes 132 us.
 #include <algorithm>
 
 #include "mx.cuh"

@@ -178,7 +178,7 @@ LINEAR_SHAPES = [(1, 128, 128), (1, 8, 256), (1, 5120, 5120), (2, 136, 384), (7,
                  (64, 512, 1024), (65, 128, 384), (115, 640, 1280), (128, 256, 512), (129, 392, 640), (255, 512, 256),
                  (256, 256, 128), (257, 520, 1152), (300, 512, 640), (515, 1160, 1920), (1000, 768, 1024),
                  (1024, 2560, 256), (2050, 136, 512), (513, 5000, 256), (512, 5120, 1152), (1800, 2200, 384),
-                 (2304, 2304, 128)]
+                 (2304, 2304, 128), (300, 8, 128), (1000, 24, 256), (5, 50000, 256), (2, 136, 65536), (300, 264, 32768)]
 
 
 @pytest.mark.parametrize("m,n,k", LINEAR_SHAPES)
@@ -201,6 +201,22 @@ def test_linear_writes_only_its_output(lib, m, n, k):
     _check_linear(y.contiguous(), a, w, None)
     out.fill_(5.0)
     assert bool((wide == 5.0).all())
+
+
+@pytest.mark.parametrize("m", [1, 40, 300])
+def test_linear_wide_exponents(lib, m):
+    """Rows and columns of very different scale, zero blocks among them: products from 2^-100 to 2^100."""
+    n, k = 264, 640
+    rng = np.random.default_rng(m)
+    x = rng.standard_normal((m, k)) * np.exp2(rng.integers(-60, 60, (m, 1)))
+    w = rng.standard_normal((n, k)) * np.exp2(rng.integers(-40, 40, (n, 1)))
+    x[:, 32:64] = 0.0
+    w[::3, 96:160] = 0.0
+    x_bits, w_bits = O.f64_to_bf16(x), O.f64_to_bf16(w)
+    qa, qw = lib.svdq_quantize_mxfp4(dev_bits(x_bits)), lib.svdq_quantize_mxfp4(dev_bits(w_bits))
+    a = O.mx4_dequantize(*O.mx_quantize_values(O.bf16_to_f64(x_bits), "mxfp4"))
+    b = O.mx4_dequantize(*O.mx_quantize_values(O.bf16_to_f64(w_bits), "mxfp4"))
+    _check_linear(lib.svdq_linear_mxfp4(qa["codes"], qa["sf"], qw["codes"], qw["sf"]), a, b, None)
 
 
 @pytest.mark.parametrize("m", [1, 20, 300])
@@ -441,3 +457,49 @@ def test_two_streams_at_once(lib):
     for g, w in zip(got, want):
         assert all(torch.equal(a, b) for a, b in zip(g, w))
     assert lib.svdq_device_error() == 0
+
+
+def test_two_host_threads(lib):
+    """Calls from two threads at once, each on a stream of its own (the binding releases the interpreter
+    lock inside the library)."""
+    import threading
+    states = [_block_state(lib, m, 1280, 170 + m) for m in (2, 300)]
+    want = [[t.clone() for t in _block(lib, s)] for s in states]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(s, w):
+        st = torch.cuda.Stream()
+        for _ in range(30):
+            got = _block(lib, s, stream=st)
+            st.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, w)):
+                bad.append(1)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(states, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and lib.svdq_device_error() == 0
+
+
+def test_refusals_on_the_device(lib):
+    """Views the kernels cannot take are refused, and the next call runs."""
+    x = torch.zeros((4, 264), dtype=torch.bfloat16, device="cuda")
+    q = lib.svdq_quantize_mxfp4(x[:, :256])
+    with pytest.raises(lib.SvdqError) as e:
+        lib.svdq_quantize_mxfp4(x[:, 4:260])                  # rows not 16-byte aligned
+    assert e.value.status == lib._lib.SVDQ_ERR_MISALIGNED
+    with pytest.raises(ValueError):
+        lib.svdq_quantize_mxfp4(x.t()[:128])                  # columns not adjacent
+    with pytest.raises(lib.SvdqError):
+        lib.svdq_linear_mxfp4(q["codes"][:0], q["sf"], q["codes"], q["sf"])
+    with pytest.raises(lib.SvdqError) as e:
+        lib.svdq_linear_mxfp4(q["codes"], q["sf"], q["codes"], q["sf"])      # N = 4
+    assert e.value.status == lib._lib.SVDQ_ERR_UNSUPPORTED
+    with pytest.raises(lib.SvdqError):
+        lib.svdq_rmsnorm_mxfp8(x[:, :256], torch.ones(256, device="cuda"), eps=0.0)
+    with pytest.raises(ValueError, match="different devices"):
+        lib.svdq_rmsnorm_mxfp8(x[:, :256], torch.ones(256))
+    _check_exact(lib.svdq_quantize_mxfp4(x[:, :256]), host_bits(x[:, :256].contiguous()))
