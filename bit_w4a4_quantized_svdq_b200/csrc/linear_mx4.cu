@@ -3,7 +3,7 @@
 //
 //   Y[m, n] = bf16( sum_k dec(A)[m, k] dec(W)[n, k] + bias[n] ),  fp32 accumulation
 //
-// Up to 128 rows (linear_mx4_few_kernel): the weight is what has to be read, K/2 + K/32
+// Up to 64 rows, and up to 128 where K is long (linear_mx4_few_kernel): the weight is what has to be read, K/2 + K/32
 // bytes a row of W.  The MMA takes 128 rows of W as its M operand and the activation rows
 // (8 to 128) as its N operand, so no tensor-core row is spent on rows that are not there.
 // A CTA owns one block of 128 weight rows and a slice of K; the slices of one block are a
@@ -172,9 +172,8 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
         const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag, args.err, kErrWaitMma));
         tc_fence_after();
         if (ok) {
-            const int64_t n = static_cast<int64_t>(n_blk) * 128 + row;
-            const float b = (splits == 1 && args.bias && n < args.N) ? bf16_lo(args.bias[n]) : 0.0f;
-            float* part = reinterpret_cast<float*>(smem);
+            // [activation row][weight row], over the ring: every copy has landed and been used
+            float* part = reinterpret_cast<float*>(smem) + row;
             constexpr int kC = kNT < 32 ? kNT : 32;
 #pragma unroll
             for (int c = 0; c < kNT; c += kC) {
@@ -184,44 +183,48 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
                 else tmem_ld_32x32b_x32(tbase + c, v);
                 tmem_ld_wait(v);
 #pragma unroll
-                for (int j = 0; j < kC; ++j) {
-                    const int64_t m = c + j;
-                    if (splits > 1) {
-                        part[(c + j) * 128 + row] = __uint_as_float(v[j]);
-                    } else if (m < args.M && n < args.N && store_ok(m * args.ldy + n, 1, args.ext_y, args.err, kSiteLinearMx4)) {
-                        args.Y[m * args.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[j]) + b));
-                    }
-                }
+                for (int j = 0; j < kC; ++j) part[(c + j) * 128] = __uint_as_float(v[j]);
             }
         }
     }
     __syncwarp();
-    if (splits > 1) {
-        // Every CTA of the cluster sums its share of the activation rows over all ranks,
-        // in rank order; a wait that ran out has set the error word and still gets here.
-        cluster_sync_all();
-        if (warp >= 2) {
-            // A warp takes activation rows of this rank in turn, a lane four weight rows of one;
-            // kAhead rows' loads are in flight at once (a remote load takes most of a microsecond).
-            constexpr int kAhead = kNT <= 8 ? 1 : 4;
-            const int64_t n = static_cast<int64_t>(n_blk) * 128 + lane * 4;
-            uint2 bb = make_uint2(0u, 0u);
-            if (args.bias && n < args.N) bb = *reinterpret_cast<const uint2*>(args.bias + n);
-            const float b[4] = {bf16_lo(bb.x), bf16_hi(bb.x), bf16_lo(bb.y), bf16_hi(bb.y)};
-            const int rows = static_cast<int>(args.M);
-            for (int t0 = rank + splits * (warp - 2); t0 < rows; t0 += splits * 4 * kAhead) {
+    // Every CTA of the cluster sums its share of the activation rows over all ranks, in
+    // rank order; a wait that ran out has set the error word and still gets here.
+    if (splits > 1) cluster_sync_all();
+    else __syncthreads();
+    if (warp >= 2) {
+        // A warp takes activation rows of this rank in turn, a lane four weight rows of one;
+        // kAhead rows' loads are in flight at once (a remote load takes most of a microsecond).
+        constexpr int kAhead = kNT <= 8 ? 1 : 4;
+        constexpr int kWarps = 4;
+        const int64_t n = static_cast<int64_t>(n_blk) * 128 + lane * 4;
+        uint2 bb = make_uint2(0u, 0u);
+        if (args.bias && n < args.N) bb = *reinterpret_cast<const uint2*>(args.bias + n);
+        const float b[4] = {bf16_lo(bb.x), bf16_hi(bb.x), bf16_lo(bb.y), bf16_hi(bb.y)};
+        const int rows = static_cast<int>(args.M);
+        auto store = [&](int t, const float4& v) {
+            const int64_t off = t * args.ldy + n;                        // N % 8 == 0: four columns or none
+            if (n < args.N && store_ok(off, 4, args.ext_y, args.err, kSiteLinearMx4))
+                *reinterpret_cast<uint2*>(args.Y + off) =
+                    make_uint2(pack_bf16x2_rn(v.x + b[0], v.y + b[1]), pack_bf16x2_rn(v.z + b[2], v.w + b[3]));
+        };
+        if (splits == 1) {
+            for (int t = warp - 2; t < rows; t += kWarps)
+                store(t, *reinterpret_cast<const float4*>(smem + t * 512 + lane * 16));
+        } else {
+            for (int t0 = rank + splits * (warp - 2); t0 < rows; t0 += splits * kWarps * kAhead) {
                 float4 s[kAhead];
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) s[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-                for (int r = 0; r < splits; r += 2) {                // splits is even; added in rank order
+                for (int r = 0; r < splits; r += 2) {            // splits is even; added in rank order
                     float4 p[2][kAhead];
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         const uint32_t src = cluster_addr(smem, r + q) + lane * 16;
 #pragma unroll
                         for (int j = 0; j < kAhead; ++j) {
-                            const int t = t0 + j * splits * 4;
+                            const int t = t0 + j * splits * kWarps;
                             p[q][j] = t < rows ? ld_cluster_f32x4(src + t * 512) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         }
                     }
@@ -235,16 +238,13 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
                 }
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) {
-                    const int t = t0 + j * splits * 4;
-                    const int64_t off = t * args.ldy + n;                    // N % 8 == 0: four columns or none
-                    if (t < rows && n < args.N && store_ok(off, 4, args.ext_y, args.err, kSiteLinearMx4))
-                        *reinterpret_cast<uint2*>(args.Y + off) =
-                            make_uint2(pack_bf16x2_rn(s[j].x + b[0], s[j].y + b[1]), pack_bf16x2_rn(s[j].z + b[2], s[j].w + b[3]));
+                    const int t = t0 + j * splits * kWarps;
+                    if (t < rows) store(t, s[j]);
                 }
             }
         }
-        cluster_sync_all();                      // no CTA leaves while its partials are being read
     }
+    if (splits > 1) cluster_sync_all();          // no CTA leaves while its partials are being read
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -272,11 +272,17 @@ int launch_few(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* w_cod
         !encode_tmap_3d_u8(&tsa, a_sf, 256, halves, (a.M + 127) / 128, 256, halves * 256, 256, 4, 1))
         return SVDQ_ERR_CUDA;
     const int64_t n_blocks = (a.N + 127) / 128;
-    // Slices of K: as many as keep every CTA resident (two per SM), at most 8 (a portable
-    // cluster).  One row, 5120 -> 5120: 4 slices 5.3 us; 2 slices 6.9, 8 slices (two waves) 9.3.
+    // Slices of K, at most 8 (a portable cluster): twice as many while every CTA stays resident
+    // (two per SM) and the slices are long enough that the halved loads (0.4 us a stage) are
+    // worth another set of partial sums, which cost more the more rows they have.  Columns
+    // 1280, us: one row, K 512: 2.8 whole, 3.0 in two; K 5120: 10.3, 6.8, 5.0, 4.6 in 1, 2, 4, 8;
+    // 32 rows, K 1280: 5.0, 4.4, 4.7 in 1, 2, 4, K 5120: 5.9 in 4, 6.3 in 8; 64 rows, K 20480: 12.9
+    // and 10.4.  One row, 5120 -> 5120: 4 slices 5.3, 8 (which do not fit at once) 9.3.
     const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 148;
     int splits = 1;
-    while (splits < 8 && n_blocks * splits * 2 <= 2 * sms && splits * 2 <= a.k_stages) splits *= 2;
+    while (splits < 8 && n_blocks * splits * 2 <= 2 * sms &&
+           a.k_stages >= (splits == 1 ? 4 : splits == 2 ? 8 : kNT == 8 ? 16 : 64))
+        splits *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(n_blocks * splits), 1, 1);
     cfg.blockDim = dim3(kFewThreads, 1, 1);
@@ -657,13 +663,15 @@ extern "C" int svdq_linear_mxfp4(const uint8_t* a_codes, const uint8_t* a_sf, co
     a.k_stages = static_cast<int>((K + kStageK - 1) / kStageK);
     a.ext_y = (M - 1) * ldy + N;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // Up to 128 rows the tile's N operand is the rows themselves (128 rows, 5120 -> 5120: 10.9 us;
-    // 129 rows in a pair's 256-row tiles 10.2, and one row there would take as long).
+    // The MMA's N operand is the rows themselves up to 64 of them, and up to 128 where K is
+    // long: a pair's 256-row tile has no partial sums to add but reads K unsliced (128 rows,
+    // 1280 -> 1280: 6.7 us sliced, 5.1 in a pair; 115 rows, 5120 -> 5120: 10.8 and 10.2, 20480 -> 5120:
+    // 17.8 and 29; 64 rows, 5120 -> 5120: 8.4 and 9.9).
     if (M <= 8) return launch_few<8>(a_codes, a_sf, w_codes, w_sf, a, st);
     if (M <= 16) return launch_few<16>(a_codes, a_sf, w_codes, w_sf, a, st);
     if (M <= 32) return launch_few<32>(a_codes, a_sf, w_codes, w_sf, a, st);
     if (M <= 64) return launch_few<64>(a_codes, a_sf, w_codes, w_sf, a, st);
-    if (M <= 128) return launch_few<128>(a_codes, a_sf, w_codes, w_sf, a, st);
+    if (M <= 128 && a.k_stages > 16) return launch_few<128>(a_codes, a_sf, w_codes, w_sf, a, st);
     // A stage takes about 600 cycles whatever the tile's width, so the narrow tile pays only
     // where it costs no further wave: there it has half the epilogue and twice the pairs at
     // work (256 x 5120 -> 5120: 10.4 against 11.9 us, 515 x 1920 -> 1160: 6.2 against 8.3;

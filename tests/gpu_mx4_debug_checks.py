@@ -66,9 +66,9 @@ def test_norm_sites(P, fmt, k):
         _check_prefix(out[key], want[key], limit * width)
 
 
-@pytest.mark.parametrize("m", [5, 100])
-def test_linear_few_rows_site(P, m):
-    n, k = 392, 1024
+@pytest.mark.parametrize("m,k", [(5, 1024), (60, 1024), (100, 8192)])   # the kernel whose M operand is the weight
+def test_linear_few_rows_site(P, m, k):
+    n = 392
     qa, qw = P.svdq_quantize_mxfp4(_x(m, k)), P.svdq_quantize_mxfp4(_x(n, k, 2))
     want = P.svdq_linear_mxfp4(qa["codes"], qa["sf"], qw["codes"], qw["sf"])
     y = _filled(torch.empty_like(want))
@@ -77,9 +77,9 @@ def test_linear_few_rows_site(P, m):
     _check_prefix(y, want, limit * 2)
 
 
-@pytest.mark.parametrize("m,n", [(300, 384), (4000, 5120)])    # 128-column and 256-column tiles
-def test_linear_many_rows_site(P, m, n):
-    k = 384
+# 128-column tiles (100 rows of a short K among them) and 256-column tiles
+@pytest.mark.parametrize("m,n,k", [(100, 384, 1024), (300, 384, 384), (4000, 5120, 384)])
+def test_linear_many_rows_site(P, m, n, k):
     qa, qw = P.svdq_quantize_mxfp4(_x(m, k)), P.svdq_quantize_mxfp4(_x(n, k, 2))
     want = P.svdq_linear_mxfp4(qa["codes"], qa["sf"], qw["codes"], qw["sf"])
     y = _filled(torch.empty_like(want))

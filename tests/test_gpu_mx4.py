@@ -178,7 +178,8 @@ LINEAR_SHAPES = [(1, 128, 128), (1, 8, 256), (1, 5120, 5120), (2, 136, 384), (7,
                  (64, 512, 1024), (65, 128, 384), (115, 640, 1280), (128, 256, 512), (129, 392, 640), (255, 512, 256),
                  (256, 256, 128), (257, 520, 1152), (300, 512, 640), (515, 1160, 1920), (1000, 768, 1024),
                  (1024, 2560, 256), (2050, 136, 512), (513, 5000, 256), (512, 5120, 1152), (1800, 2200, 384),
-                 (2304, 2304, 128), (300, 8, 128), (1000, 24, 256), (5, 50000, 256), (2, 136, 65536), (300, 264, 32768)]
+                 (2304, 2304, 128), (300, 8, 128), (1000, 24, 256), (5, 50000, 256), (2, 136, 65536), (300, 264, 32768),
+                 (100, 264, 4096), (100, 264, 4224), (60, 20000, 512), (128, 20000, 4352), (16, 1160, 16384)]
 
 
 @pytest.mark.parametrize("m,n,k", LINEAR_SHAPES)
