@@ -44,6 +44,8 @@ __global__ void __launch_bounds__(kThreads)
 mx4_quantize_kernel(const MxArgs a) {
     const int lane = threadIdx.x & 31, sub = lane & 7;
     const uint32_t u0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnitsPerWarp;
+    pdl_launch_dependents();
+    pdl_wait();                                 // the kernel before has written what this one reads
     uint32_t v[kUnroll][8];
     int64_t row[kUnroll];
     uint32_t atom[kUnroll];
@@ -104,6 +106,8 @@ mx_dequantize_kernel(const MxArgs a) {
     constexpr int kWords = kFmt == kMxFp8 ? 4 : 2;          // 16 codes
     const int lane = threadIdx.x & 31, sub = lane & 7;
     const uint32_t u0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kUnitsPerWarp;
+    pdl_launch_dependents();
+    pdl_wait();                                 // the kernel before has written what this one reads
     uint32_t q[kUnroll][kWords], sb[kUnroll];
     int64_t row[kUnroll], col[kUnroll];
 #pragma unroll
@@ -169,9 +173,19 @@ int mx_prepare(const void* v, int64_t M, int64_t K, int64_t ldx, const uint8_t* 
     return SVDQ_OK;
 }
 
-unsigned mx_grid(uint32_t units) {
+template <typename Kernel>
+int mx_launch(Kernel kern, const MxArgs& a, void* stream) {
     constexpr uint32_t per_block = (kThreads / 32) * kUnitsPerWarp;
-    return (units + per_block - 1) / per_block;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.n_units + per_block - 1) / per_block, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return launch_status(cudaLaunchKernelEx(&cfg, kern, a));
 }
 
 template <int kFmt>
@@ -181,8 +195,7 @@ int mx_dequantize(const uint8_t* codes, const uint8_t* sf, int64_t M, int64_t K,
     if (st != SVDQ_OK) return st;
     a.y = static_cast<uint16_t*>(Y);
     a.ext_y = debug_extent(kSiteMxValues, (M - 1) * ldy + K);
-    mx_dequantize_kernel<kFmt><<<mx_grid(a.n_units), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return launch_status(cudaGetLastError());
+    return mx_launch(mx_dequantize_kernel<kFmt>, a, stream);
 }
 
 }  // namespace
@@ -199,8 +212,7 @@ extern "C" int svdq_quantize_mxfp4(const void* X, int64_t M, int64_t K, int64_t 
     a.x = static_cast<const uint16_t*>(X);
     a.ext_codes = debug_extent(kSiteMxCodes, M * K / 2);
     a.ext_sf = debug_extent(kSiteMxSf, static_cast<int64_t>(svdq_mxfp4_sf_bytes(M, K)));
-    mx4_quantize_kernel<<<mx_grid(a.n_units), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return launch_status(cudaGetLastError());
+    return mx_launch(mx4_quantize_kernel, a, stream);
 }
 
 extern "C" int svdq_dequantize_mxfp4(const uint8_t* codes, const uint8_t* sf, int64_t M, int64_t K, void* Y, int64_t ldy,

@@ -554,8 +554,8 @@ def svdq_linear_mxfp4(a_codes: torch.Tensor, a_sf: torch.Tensor, w_codes: torch.
     elif out.dtype not in _BF16_TYPES or out.shape != (m, n):
         raise ValueError(f"out must be a bf16 [{m}, {n}] tensor")
     _lib.check("svdq_linear_mxfp4", lib.svdq_linear_mxfp4(
-        _ptr(a_codes), _ptr(a_sf), _ptr(w_codes), _ptr(w_sf), _ptr(bias), _ptr(out), _row_stride(out, "out"),
-        m, n, k, _stream(stream)))
+        a_codes.data_ptr(), a_sf.data_ptr(), w_codes.data_ptr(), w_sf.data_ptr(), _ptr(bias), out.data_ptr(),
+        _row_stride(out, "out"), m, n, k, _stream(stream)))
     return out
 
 
@@ -563,28 +563,31 @@ def _rmsnorm_mx(name: str, x, weight, residual, eps: float, per_byte: int, out, 
     lib = _lib.load()
     _check_bf16(x, "x")
     m, k = x.shape
-    _check_dense(weight, (*_BF16_TYPES, torch.float32), 0, "weight")
+    _check_dense(weight, (torch.bfloat16, torch.float32, torch.int16, torch.uint16), 0, "weight")
     if weight.numel() != k:
         raise ValueError(f"weight holds {weight.numel()} elements, a row of x {k}")
-    if residual is not None:
-        _check_bf16(residual, "residual")
-        if residual.shape != (m, k):
-            raise ValueError(f"residual must be [{m}, {k}], got {list(residual.shape)}")
     h = None if out is None else out.get("h")
-    codes = _mx_outputs(out, m, k, k // per_byte, x.device)
     if residual is None:
         if h is not None:
             raise ValueError("out['h'] is the sum with a residual, and there is none")
-    elif h is None:
-        h = _lib.out_empty((m, k), torch.bfloat16, x.device)
-    if h is not None and (h.dtype not in _BF16_TYPES or h.shape != (m, k)):
-        raise ValueError(f"out['h'] must be a bf16 [{m}, {k}] tensor")
+        r_ptr = h_ptr = None
+        ldr = ldh = 0
+    else:
+        _check_bf16(residual, "residual")
+        if residual.shape != (m, k):
+            raise ValueError(f"residual must be [{m}, {k}], got {list(residual.shape)}")
+        if h is None:
+            h = _lib.out_empty((m, k), torch.bfloat16, x.device)
+        elif h.dtype not in _BF16_TYPES or h.shape != (m, k):
+            raise ValueError(f"out['h'] must be a bf16 [{m}, {k}] tensor")
+        r_ptr, h_ptr = residual.data_ptr(), h.data_ptr()
+        ldr, ldh = _row_stride(residual, "residual"), _row_stride(h, "out['h']")
+    q = _mx_outputs(out, m, k, k // per_byte, x.device)
+    codes, sf = q["codes"], q["sf"]
     _lib.check(name, getattr(lib, name)(
-        _ptr(x), m, k, _row_stride(x, "x"), _ptr(residual),
-        0 if residual is None else _row_stride(residual, "residual"), _ptr(weight),
-        1 if weight.dtype == torch.float32 else 0, float(eps), _ptr(h), 0 if h is None else _row_stride(h, "out['h']"),
-        _ptr(codes["codes"]), _ptr(codes["sf"]), _stream(stream)))
-    return dict(codes=codes["codes"], sf=codes["sf"], h=h)
+        x.data_ptr(), m, k, _row_stride(x, "x"), r_ptr, ldr, weight.data_ptr(), 1 if weight.dtype is torch.float32 else 0,
+        eps, h_ptr, ldh, codes.data_ptr(), sf.data_ptr(), _stream(stream)))
+    return dict(codes=codes, sf=sf, h=h)
 
 
 @_on_tensor_device
