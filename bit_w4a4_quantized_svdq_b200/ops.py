@@ -8,6 +8,12 @@ Every call runs on the device that holds its tensors: all tensor arguments
 must share one CUDA device, which is made current for the call (the library
 looks up its per-device state -- error word, SM count, static arrays -- on the
 current device), and the default stream is that device's current stream.
+
+A call given a stream runs there and takes its new outputs from that stream's
+pool.  The caller waits for that stream before it reads them on another.  Both
+the given stream and the one current at the call may hold unfinished work on an
+output when it is released; a third stream is announced with the tensor's
+``record_stream``, as for any torch tensor.
 """
 from __future__ import annotations
 
@@ -61,10 +67,19 @@ def _on_tensor_device(fn):
         if stream is not None and stream.device != dev:
             raise ValueError(f"{fn.__name__}: stream is on {stream.device}, tensors on {dev}")
         if stream is not None:
-            # outputs come from that stream's pool: memory freed after the call is not handed
-            # to another stream while this call's kernels still use it
+            # outputs and workspaces come from that stream's pool: memory freed after the call
+            # is not handed to another stream while this call's kernels still use it
+            caller = torch.cuda.current_stream(dev)
             with torch.cuda.stream(stream):
-                return fn(*args, **kwargs)
+                out = fn(*args, **kwargs)
+            if caller != stream:
+                # the calling stream reads the outputs once it has waited for `stream`: their
+                # memory, released, must not go to a later call before those reads are done
+                given = {id(t) for a in (*args, *kwargs.values()) for t in _tensors_in(a)}
+                for t in _tensors_in(out):
+                    if id(t) not in given:
+                        t.record_stream(caller)
+            return out
         with torch.cuda.device(dev):
             return fn(*args, **kwargs)
 
