@@ -244,6 +244,7 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
             }
         }
     }
+    __syncwarp();                                // lanes past N skipped their stores; the barrier takes whole warps
     if (splits > 1) cluster_sync_all();          // no CTA leaves while its partials are being read
     tc_fence_before();
     __syncthreads();
@@ -527,6 +528,7 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
             uint16_t* bt = bias_s + (t & 1) * 256;
             const int64_t bn = static_cast<int64_t>(n_blk) * kN + etid;
             bt[etid] = (args.g.bias && etid < kN && bn < args.g.N) ? args.g.bias[bn] : static_cast<uint16_t>(0);
+            __syncwarp();                                     // the barrier takes whole warps
             if (bar_sync_or<1, kPairEpiWarps * 32>(*abort_flag != 0u)) break;
             if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[t & 1], (t >> 1) & 1, abort_flag, err, kErrWaitMma))) continue;
             tc_fence_after();
@@ -571,6 +573,7 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                     tma_store_2d_hint(&tmap_y, box, static_cast<int32_t>(x), row0, pol_y);
                     bulk_commit_group();
                 }
+                __syncwarp();                                        // the next read of tensor memory takes the whole warp
             }
         }
         if (lane == 0) bulk_wait_all();
