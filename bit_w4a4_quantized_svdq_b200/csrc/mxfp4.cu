@@ -117,12 +117,12 @@ mx_dequantize_kernel(const MxArgs a) {
         row[i] = r;
         col[i] = static_cast<int64_t>(t) * kMxAtomK + sub * 16;
         if (u < a.n_units) {
-            sb[i] = __ldg(a.sf + mx_sf_word(row[i], t, a.atoms.d) + (sub >> 1));
+            sb[i] = ld_global_u8(a.sf + mx_sf_word(row[i], t, a.atoms.d) + (sub >> 1));
             if constexpr (kFmt == kMxFp8) {
-                const uint4 w = ldg_stream_v4(a.codes + row[i] * a.K + col[i]);
+                const uint4 w = ld_global_once_v4(a.codes + row[i] * a.K + col[i]);
                 q[i][0] = w.x; q[i][1] = w.y; q[i][2] = w.z; q[i][3] = w.w;
             } else {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.codes + (row[i] * a.K + col[i]) / 2));
+                const uint2 w = ld_global_v2(a.codes + (row[i] * a.K + col[i]) / 2);
                 q[i][0] = w.x; q[i][1] = w.y;
             }
         }

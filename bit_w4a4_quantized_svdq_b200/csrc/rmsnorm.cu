@@ -70,7 +70,7 @@ template <bool kW32>
 __device__ __forceinline__ void load_weight16(const void* weight, int64_t c, uint64_t (&wv)[8]) {
 #pragma unroll
     for (int j = 0; j < (kW32 ? 4 : 2); ++j) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(weight) + c / (kW32 ? 4 : 8) + j);
+        const uint4 w = ld_global_v4(static_cast<const uint8_t*>(weight) + c * (kW32 ? 4 : 2) + 16 * j);
         if constexpr (kW32) {
             wv[2 * j] = pack_f32x2(__uint_as_float(w.x), __uint_as_float(w.y));
             wv[2 * j + 1] = pack_f32x2(__uint_as_float(w.z), __uint_as_float(w.w));
