@@ -133,20 +133,12 @@ _GUARD_FILL = 0xA5
 _guarded = []
 
 
-# torch's allocation of a strided tensor on the current device without the argument
-# parsing of torch.empty (0.8 against 1.6 us, where an output's call takes 11 to 17), where
-# this torch has it.
-_empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
-
-
 def out_empty(shape, dtype, device):
     """Output buffer of a call (whose device is current): torch.empty, or in debug mode a
     guarded view (plain torch.empty while a CUDA graph is being captured)."""
     shape = (shape,) if isinstance(shape, int) else tuple(shape)
     if not DEBUG or torch.cuda.is_current_stream_capturing():
-        if _empty_cuda is not None and device.type == "cuda" and len(shape) <= 2:
-            return _empty_cuda(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
-        return torch.empty(*shape, dtype=dtype, device=device)   # sizes one by one: parsed faster than a tuple
+        return torch.empty(shape, dtype=dtype, device=device)
     n = 1
     for d in shape:
         n *= int(d)
