@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from ctypes import POINTER, Structure, c_char_p, c_float, c_int, c_int64, c_size_t, c_uint32, c_void_p
 
 import torch
@@ -131,6 +132,10 @@ def check(call: str, status: int) -> None:
 _GUARD = 4096
 _GUARD_FILL = 0xA5
 _guarded = []
+# Held over a whole call in debug mode (allocation, launch, check), by every host thread: the
+# list above and the device error word are the process's, and one thread's check would
+# otherwise take another's unfinished buffers and clear its error.
+debug_lock = threading.RLock()
 
 
 def out_empty(shape, dtype, device):

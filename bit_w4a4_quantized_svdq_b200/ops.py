@@ -100,7 +100,15 @@ def _on_tensor_device(fn):
             return refuse_or_run(args, kwargs)
         return fn(*args, **kwargs)
 
-    return wrapper
+    if not _lib.DEBUG:
+        return wrapper
+
+    @functools.wraps(fn)
+    def one_at_a_time(*args, **kwargs):
+        with _lib.debug_lock:
+            return wrapper(*args, **kwargs)
+
+    return one_at_a_time
 
 
 def _ptr(t: Optional[torch.Tensor]):
