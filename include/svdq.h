@@ -391,7 +391,12 @@ int svdq_linear_mxfp8(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t
  * written); it must not overlap them otherwise.  weight: [K], weight_dtype 0 = bf16,
  * 1 = fp32, 16-byte aligned.  eps > 0, finite.  codes and sf as the quantisers write
  * them.  A row that holds an infinity or a NaN follows IEEE arithmetic: E4M3 NaN
- * codes, or NaN block scales in MXFP4.  K % 128 == 0, M >= 1.
+ * codes, or NaN block scales in MXFP4.  Where h * rstd * weight leaves fp32's range,
+ * or an infinite weight meets h != 0, y is an infinity: MXFP4 gives its block the NaN
+ * scale; MXFP8 gives the block scale byte 247 (2^120) and the element the largest
+ * code of its sign, 448, whose value 448 * 2^120 svdq_dequantize_mxfp8 returns as an
+ * infinity, and the block's elements below 2^110 become zero.  An infinite weight
+ * on h = 0 is a NaN.  K % 128 == 0, M >= 1.
  *
  * All are asynchronous on `stream`.
  */
