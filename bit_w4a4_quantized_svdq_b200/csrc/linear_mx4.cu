@@ -133,6 +133,12 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
                 tma_load_3d(st + L::kW + L::kA + kSfAtoms, &tmap_sfa, &full[s], 0, kb * 4, 0);
                 if (++s == L::kStages) { s = 0; ph ^= 1u; }
             }
+            // Every slot free again: the last stages' commits have arrived while this CTA's
+            // barriers exist (the one the epilogue waits for is another, and unordered with them).
+            for (int i = 0; i < L::kStages; ++i) {
+                if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, args.err, kErrWaitEmpty)) break;
+                if (++s == L::kStages) { s = 0; ph ^= 1u; }
+            }
             // Bounded drain: a copy may still be in flight where a wait ran out.
             for (int i = (it > L::kStages ? it - L::kStages : 0); i < it; ++i) {
                 const long long t0 = clock64();
@@ -434,6 +440,12 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                     tma_load_2d_pair(st + L::kA, &tmap_w, bar, kb * 128, n_blk * kN + rank * (kN / 2), pol_w);
                     if (++s == L::kStages) { s = 0; ph ^= 1u; }
                 }
+            }
+            // Every slot free again, in both CTAs: the first CTA's commits for the last stages
+            // have arrived here (acc_full's, which the epilogue waits for, is unordered with them).
+            for (int i = 0; i < L::kStages && ok; ++i) {
+                ok = mbar_wait(&empty[s], ph ^ 1, abort_flag, err, kErrWaitEmpty);
+                if (++s == L::kStages) { s = 0; ph ^= 1u; }
             }
             if (!ok) {                                        // a wait ran out: let the copies in flight land (~1 ms)
                 const long long t0 = clock64();
