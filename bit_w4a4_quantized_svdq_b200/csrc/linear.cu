@@ -241,15 +241,16 @@ __device__ __forceinline__ bool lr_stage(const LinearArgs& a, uint8_t* slot, uin
         const float4* src = reinterpret_cast<const float4*>(a.D + gm * r + 16 * h);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float4 v = __ldg(src + q);
-            dv[4 * q] = v.x; dv[4 * q + 1] = v.y; dv[4 * q + 2] = v.z; dv[4 * q + 3] = v.w;
+            const uint4 v = ld_global_v4(src + q);
+            dv[4 * q] = __uint_as_float(v.x); dv[4 * q + 1] = __uint_as_float(v.y);
+            dv[4 * q + 2] = __uint_as_float(v.z); dv[4 * q + 3] = __uint_as_float(v.w);
         }
     }
     uint4 u[4];                                              // B row etid: up[n, 0..31] (zero past r)
     const int64_t gn = static_cast<int64_t>(n_blk) * kBN + etid;
     const uint4* usrc = reinterpret_cast<const uint4*>(a.up + gn * r);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) u[c] = (c * 8 < r && gn < a.N) ? __ldg(usrc + c) : make_uint4(0, 0, 0, 0);
+    for (int c = 0; c < 4; ++c) u[c] = (c * 8 < r && gn < a.N) ? ld_global_v4(usrc + c) : make_uint4(0, 0, 0, 0);
     // D' = D / alpha as bf16 hi + lo pairs, formed before the wait
     uint32_t hi[8], lo[8];
 #pragma unroll
@@ -640,7 +641,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
         int2* segrows = reinterpret_cast<int2*>(segsum + kMaxSegments);  // [segment] rows [begin, end)
         const int n_seg = args.segs.n;
         pdl_wait();                                   // inputs of the earlier kernels are written
-        const float alpha = __fmul_rn(__ldg(args.s_g_act), __ldg(args.s_g_w));
+        const float alpha = __fmul_rn(ld_global_f32(args.s_g_act), ld_global_f32(args.s_g_w));
         const float inv_alpha = __frcp_rn(alpha);
         for (int i = etid; i < kMaxSegments; i += kEpiWarps * 32) {
             segsum[i] = make_double2(0.0, 0.0);
@@ -845,7 +846,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
         uint8_t* stg = smem + L::kOffEpi + ew * kYStageBytes;
         const uint64_t pol_y = l2_evict_first_policy();
         pdl_wait();                                   // inputs of the earlier kernels are written
-        const float alpha = kMx ? 1.0f : __fmul_rn(__ldg(args.s_g_act), __ldg(args.s_g_w));
+        const float alpha = kMx ? 1.0f : __fmul_rn(ld_global_f32(args.s_g_act), ld_global_f32(args.s_g_w));
         const float inv_alpha = __frcp_rn(alpha);
         // the first tile's low-rank stage (ring position 0); a failure raises the
         // abort flag, which the loop top reads

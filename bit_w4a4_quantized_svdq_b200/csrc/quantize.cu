@@ -256,13 +256,13 @@ quantize_act_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_con
         pdl_wait();                               // the tensor scale is written
         if (threadIdx.x < 128) {
             // 1/S for every scale byte the RNE-satfinite conversion can produce (0x00..0x7E).
-            const float s_g0 = __ldg(args.s_g);
+            const float s_g0 = ld_global_f32(args.s_g);
             const float S = __fmul_rn(e4m3_to_f32(threadIdx.x), s_g0);
             reinterpret_cast<float*>(smem + L::kTabOff)[threadIdx.x] =
                 (threadIdx.x == 0x7F || S == 0.0f) ? 0.0f : __frcp_rn(S);
         }
         asm volatile("bar.sync 1, %0;" :: "n"(kQuantWarps * 32) : "memory");
-        const float s_g = __ldg(args.s_g);
+        const float s_g = ld_global_f32(args.s_g);
         const float d = __fmul_rn(6.0f, s_g);
         const float rd = __frcp_rn(d);
         const int64_t M = args.M;
