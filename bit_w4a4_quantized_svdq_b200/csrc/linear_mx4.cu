@@ -175,6 +175,7 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        pdl_wait();                                  // bias may come from the kernel before
         const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, abort_flag, args.err, kErrWaitMma));
         tc_fence_after();
         if (ok) {
