@@ -155,8 +155,8 @@ int mx_prepare(const void* v, int64_t M, int64_t K, int64_t ldx, const uint8_t* 
     if (!aligned16(v) || (ldx * 2) % 16 != 0 || !aligned16(codes) || (reinterpret_cast<uintptr_t>(sf) & 3u))
         return SVDQ_ERR_MISALIGNED;
     const int64_t rows = pad_rows ? (M + 127) / 128 * 128 : M;
+    if (rows > 0x7FFF0000LL / (K / kMxAtomK)) return SVDQ_ERR_UNSUPPORTED;
     const int64_t units = rows * (K / kMxAtomK);
-    if (units > 0x7FFF0000LL) return SVDQ_ERR_UNSUPPORTED;
     if (!device_is_sm100()) return SVDQ_ERR_NO_DEVICE;
     if (!debug_ptrs_ok({v, codes, sf})) return SVDQ_ERR_INVALID_ARG;
     *a = MxArgs{};

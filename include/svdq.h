@@ -359,6 +359,7 @@ int svdq_linear_mxfp8(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t
  * magnitudes above 6 saturate, sign kept.  E2M1 has no NaN and no infinity: a block
  * that holds either gets scale byte 255 (the E8M0 NaN) and zero codes, which makes
  * every product with it NaN.  Pad rows of the scale layout get 0.  K % 128 == 0
+ * and at most 2^31 - 2^16 groups of 128 channels over the padded rows
  * (SVDQ_ERR_UNSUPPORTED otherwise), M >= 1.  X may lie anywhere in a larger buffer;
  * 32-byte aligned rows are read faster.
  *
@@ -366,7 +367,7 @@ int svdq_linear_mxfp8(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t
  * stride ldy >= K, ldy * 2 a multiple of 16, 16-byte aligned) = bf16(dec(code) *
  * 2^(scale - 127)), the product exact, rounded once; NaN where the scale byte is 255
  * or the E4M3 code is NaN.  Codes and sf as the quantisers of the format write them
- * (sf 4-byte aligned).
+ * (sf 4-byte aligned).  The quantiser's limits, the groups counted over M rows.
  *
  * svdq_linear_mxfp4 -- Y[m, n] = bf16( sum_k dec(A)[m, k] dec(W)[n, k] + bias[n] ),
  * dec(v) = E2M1(v) * 2^(scale - 127), fp32 accumulation on the tensor cores (tcgen05
