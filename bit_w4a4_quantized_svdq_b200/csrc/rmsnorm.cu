@@ -20,6 +20,7 @@
 //   MXFP4 92; 4096 x 5120 27 us; one row 2.5 us; 16384 x 20480 (two passes) 453-477 us.
 //   Without the next row's loads ahead 16384 x 5120 takes 132 us.
 #include <algorithm>
+#include <cfloat>
 
 #include "mx.cuh"
 
@@ -304,7 +305,7 @@ int rmsnorm_mx(const void* X, int64_t M, int64_t K, int64_t ldx, const void* res
     if ((residual != nullptr) != (H != nullptr)) return SVDQ_ERR_INVALID_ARG;
     if (M < 1 || K < 1 || ldx < K || (residual && (ldr < K || ldh < K))) return SVDQ_ERR_INVALID_ARG;
     if (weight_dtype != 0 && weight_dtype != 1) return SVDQ_ERR_INVALID_ARG;
-    if (!(eps > 0.0f) || eps > 3.0e38f) return SVDQ_ERR_INVALID_ARG;
+    if (!(eps > 0.0f) || eps > FLT_MAX) return SVDQ_ERR_INVALID_ARG;
     if (K % kMxAtomK != 0 || K > (int64_t(1) << 30) || M > (int64_t(1) << 40)) return SVDQ_ERR_UNSUPPORTED;
     if (!aligned16(X) || (ldx * 2) % 16 != 0 || !aligned16(weight) || !aligned16(codes) ||
         (reinterpret_cast<uintptr_t>(sf) & 3u))

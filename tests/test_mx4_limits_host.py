@@ -30,3 +30,14 @@ def test_sizes_past_the_unit_count_are_refused(name, m, k):
 @pytest.mark.parametrize("m,k", [(1, 128), (128, 1 << 30), (0x7FFF0000, 128), (110000, 20480)])
 def test_sizes_within_it_are_taken(name, m, k):
     assert _mx(name, m, k, k) in OK
+
+
+@pytest.mark.parametrize("name", ["svdq_rmsnorm_mxfp8", "svdq_rmsnorm_mxfp4"])
+def test_norm_takes_any_positive_finite_eps(name):
+    def call(eps):
+        return getattr(_lib.load(), name)(P, 4, 256, 256, None, 0, P, 1, eps, None, 0, P, P, None)
+
+    for eps in (1e-45, 1e-38, 1e-6, 1.0, 3.2e38, 3.4028234e38):
+        assert call(eps) in OK, eps
+    for eps in (0.0, -0.0, -1e-6, float("inf"), float("-inf"), float("nan"), 1e-46):
+        assert call(eps) == _lib.SVDQ_ERR_INVALID_ARG, eps
