@@ -42,6 +42,14 @@ __device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi) {
     return out;
 }
 
+// A bounded wait for a commit's arrival.  The loading threads use it for the last commits of every
+// ring slot: no arrival may reach a barrier whose CTA has left, and the commit that the epilogue
+// waits for is another, unordered with these.
+__device__ __forceinline__ void wait_arrival(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity) && *abort_flag == 0u && clock64() - t0 < kWaitLimitCycles) {}
+}
+
 struct Mx4Args {
     const uint16_t* bias;
     uint16_t* Y;
@@ -133,16 +141,13 @@ linear_mx4_few_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_c
                 tma_load_3d(st + L::kW + L::kA + kSfAtoms, &tmap_sfa, &full[s], 0, kb * 4, 0);
                 if (++s == L::kStages) { s = 0; ph ^= 1u; }
             }
-            // Every slot free again: the last stages' commits have arrived while this CTA's
-            // barriers exist (the one the epilogue waits for is another, and unordered with them).
-            for (int i = 0; i < L::kStages; ++i) {
-                if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, args.err, kErrWaitEmpty)) break;
-                if (++s == L::kStages) { s = 0; ph ^= 1u; }
-            }
-            // Bounded drain: a copy may still be in flight where a wait ran out.
+            // Bounded drain: a copy may still be in flight where a wait ran out, and the last stages'
+            // commits have to arrive while this CTA is here (0.2 us of a one-row call).
             for (int i = (it > L::kStages ? it - L::kStages : 0); i < it; ++i) {
                 const long long t0 = clock64();
-                while (!mbar_try_wait(&full[i % L::kStages], (i / L::kStages) & 1) && clock64() - t0 < kWaitLimitCycles) {}
+                while (!mbar_try_wait(&full[i % L::kStages], (i / L::kStages) & 1) &&
+                       clock64() - t0 < kWaitLimitCycles) {}
+                wait_arrival(&empty[i % L::kStages], (i / L::kStages) & 1, abort_flag);
             }
         }
     } else if (warp == 1) {
@@ -442,11 +447,12 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                     if (++s == L::kStages) { s = 0; ph ^= 1u; }
                 }
             }
-            // Every slot free again, in both CTAs: the first CTA's commits for the last stages
-            // have arrived here (acc_full's, which the epilogue waits for, is unordered with them).
-            for (int i = 0; i < L::kStages && ok; ++i) {
-                ok = mbar_wait(&empty[s], ph ^ 1, abort_flag, err, kErrWaitEmpty);
-                if (++s == L::kStages) { s = 0; ph ^= 1u; }
+            if (ok) {                                         // the first CTA's commits arrive in both
+#pragma unroll 1
+                for (int i = 0; i < L::kStages; ++i) {
+                    wait_arrival(&empty[s], ph ^ 1, abort_flag);
+                    if (++s == L::kStages) { s = 0; ph ^= 1u; }
+                }
             }
             if (!ok) {                                        // a wait ran out: let the copies in flight land (~1 ms)
                 const long long t0 = clock64();
