@@ -3,9 +3,10 @@
 //
 //   Y[m, n] = bf16( sum_k dec(A)[m, k] dec(W)[n, k] + bias[n] ),  fp32 accumulation
 //
-// Up to 64 rows, and up to 128 where K is long (linear_mx4_few_kernel): the weight is what has to be read, K/2 + K/32
-// bytes a row of W.  The MMA takes 128 rows of W as its M operand and the activation rows
-// (8 to 128) as its N operand, so no tensor-core row is spent on rows that are not there.
+// Up to 64 rows, and up to 128 where K is long (linear_mx4_few_kernel): the weight is what
+// has to be read, K/2 + K/32 bytes a row of W.  The MMA takes 128 rows of W as its M operand
+// and the activation rows (8 to 128) as its N operand, so no tensor-core row is spent on rows
+// that are not there.
 // A CTA owns one block of 128 weight rows and a slice of K; the slices of one block are a
 // cluster, whose partial sums meet over distributed shared memory in rank order (no
 // workspace, no atomics: bitwise repeatable).  One row, 5120 -> 5120: 5.3 us (14 MB; 2.1 us
@@ -19,10 +20,12 @@
 // scales into tensor memory, eight read the accumulator out.
 //   16384 x 20480 -> 5120  570-600 us (6.0-5.7 PFLOP/s), 650 in a loop that runs into the power limit
 //   4096 x 5120 -> 15360   117-120 us (5.5-5.4), 4096 x 5120 -> 5120  43 us (5.0; 4.3 waves of tiles)
-// What paces a stage of 256 x 256 x 256, in SM cycles: its MMAs alone 526, its copies alone
-// 448, both 588, with the scales 606 (a tile 128 columns wide: 355, 402, 572, 593; neither the
-// number of copies nor a deeper ring changes that); 800 more at a tile's end, of which the
-// wait for the shared accumulator columns is 620.
+// What paces a stage of 256 x 256 x 256, in SM cycles on 16384 x 20480 -> 5120 (80 stages a
+// tile), launches 50 ms apart: its MMAs alone 526, its copies alone 448, both 588, with the
+// scales 606 (a tile 128 columns wide: 355, 402, 572, 593; neither the number of copies nor a
+// deeper ring changes that); 800 more at a tile's end, of which the wait for the shared
+// accumulator columns is 620.  Back to back for two seconds a stage takes 636; on 4096 x 5120
+// -> 15360 (20 stages a tile) 703 apart and 736 back to back.
 // The scales do not go by tcgen05.cp: a copy holds the MMA behind it up by about 45 cycles,
 // six a stage (805 us on the first shape), and between the MMAs or a stage ahead it is no
 // better (876, 838).
@@ -316,13 +319,13 @@ int launch_few(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* w_cod
 // ---------------------------------------------------------------------------
 // Many rows
 // ---------------------------------------------------------------------------
-constexpr int kPairThreads = 448;                // warps: 0..3 scale writers, 4..11 epilogue, 12 producer, 13 MMA issuer
+constexpr int kPairThreads = 448;    // warps: 0..3 scale writers, 4..11 epilogue, 12 producer, 13 MMA issuer
 constexpr int kPairSfWarps = 4;
 constexpr int kPairEpiWarp0 = 4;
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairLoadWarp = 12;
 constexpr int kPairMmaWarp = 13;
-static_assert(kPairEpiWarp0 % 4 == 0, "each group of four warps covers the four tensor-memory lane quarters (warp % 4)");
+static_assert(kPairEpiWarp0 % 4 == 0, "four warps cover the four tensor-memory lane quarters (warp % 4)");
 constexpr uint32_t kPairTmem = 512;
 constexpr int kTileM = 256;                      // rows of a pair's tile; columns kN: 256 or 128
 
@@ -333,8 +336,8 @@ struct PairLayout {
     static constexpr uint32_t kA = 128 * 128, kB = kN / 2 * 128;            // this CTA's half of each
     static constexpr uint32_t kOffSfa = kA + kB, kOffSfb = kOffSfa + kSfAtoms;
     static constexpr uint32_t kStage = kOffSfb + kSfbBlocks * kSfAtoms;     // 35 or 26 KB
-    static constexpr uint32_t kOffOut = kStages * kStage;                   // one box of 32 rows x 64 bf16 columns per epilogue warp
-    static constexpr uint32_t kBox = 32 * 128;
+    static constexpr uint32_t kOffOut = kStages * kStage;                   // a box per epilogue warp:
+    static constexpr uint32_t kBox = 32 * 128;                              // 32 rows x 64 bf16 columns
     static constexpr uint32_t kOffBar = kOffOut + kPairEpiWarps * kBox;
     static constexpr uint32_t kOffBias = kOffBar + 256;                     // 2 x 256 bf16
     static constexpr uint32_t kBytes = kOffBias + 2 * 256 * 2;
@@ -511,7 +514,8 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                 const uint32_t base = tq + s * L::kSfCols;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    tmem_st_32x32b_x1(base + 4 * i + warp, *reinterpret_cast<const uint32_t*>(sfa + i * 512 + lane * 16 + warp * 4));
+                    tmem_st_32x32b_x1(base + 4 * i + warp,
+                                      *reinterpret_cast<const uint32_t*>(sfa + i * 512 + lane * 16 + warp * 4));
                     const uint32_t dst = base + 8 + kN / 32 * i;
                     const uint4 x = *reinterpret_cast<const uint4*>(sfb + i * 512 + lane * 16);
                     if constexpr (kN == 128) {
@@ -549,7 +553,8 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
             bt[etid] = (args.g.bias && etid < kN && bn < args.g.N) ? args.g.bias[bn] : static_cast<uint16_t>(0);
             __syncwarp();                                     // the barrier takes whole warps
             if (bar_sync_or<1, kPairEpiWarps * 32>(*abort_flag != 0u)) break;
-            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[t & 1], (t >> 1) & 1, abort_flag, err, kErrWaitMma))) continue;
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[t & 1], (t >> 1) & 1, abort_flag, err, kErrWaitMma)))
+                continue;
             tc_fence_after();
             const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ((t & 1) ? L::kAcc1 : 0u);
             const int32_t row0 = m_blk * kTileM + rank * 128 + quarter * 32;
@@ -582,7 +587,8 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                         o[j] = pack_bf16x2_rn(__uint_as_float(w[0]) + bf16_lo(bb), __uint_as_float(w[1]) + bf16_hi(bb));
                     }
                     // 128-byte swizzle: 16-byte piece c of row r sits at c ^ (r % 8)
-                    *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 fence_async_shared();
                 __syncwarp();
@@ -592,7 +598,7 @@ linear_mx4_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_
                     tma_store_2d_hint(&tmap_y, box, static_cast<int32_t>(x), row0, pol_y);
                     bulk_commit_group();
                 }
-                __syncwarp();                                        // the next read of tensor memory takes the whole warp
+                __syncwarp();                                // the next read of tensor memory takes the whole warp
             }
         }
         if (lane == 0) bulk_wait_all();

@@ -14,10 +14,10 @@
 // scale per element.  Eight lanes take a unit of 128 channels, 16 elements (one
 // 256-bit access) a lane; units are consecutive along the rows, so a warp reads 1 KB
 // contiguous per step and keeps kUnroll of them in flight.  Each warp does that once:
-// with a persistent grid of 8 CTAs an SM the loads and stores of the CTAs ran in step (16384
-// x 20480: quantiser 147 -> 140 us, read-back 146 -> 127 us, which is the copy rate).  One lane of eight writes
-// the unit's four scale bytes as one word.  Rows from M to the layout's 128-row
-// padding get zero scales.
+// with a persistent grid of 8 CTAs an SM the loads and stores of the CTAs ran in step
+// (16384 x 20480: quantiser 147 -> 140 us, read-back 146 -> 127 us, which is the copy
+// rate).  One lane of eight writes the unit's four scale bytes as one word.  Rows from M
+// to the layout's 128-row padding get zero scales.
 #include "mx.cuh"
 
 namespace svdq {
@@ -215,12 +215,12 @@ extern "C" int svdq_quantize_mxfp4(const void* X, int64_t M, int64_t K, int64_t 
     return mx_launch(mx4_quantize_kernel, a, stream);
 }
 
-extern "C" int svdq_dequantize_mxfp4(const uint8_t* codes, const uint8_t* sf, int64_t M, int64_t K, void* Y, int64_t ldy,
-                                     void* stream) {
+extern "C" int svdq_dequantize_mxfp4(const uint8_t* codes, const uint8_t* sf, int64_t M, int64_t K, void* Y,
+                                     int64_t ldy, void* stream) {
     return svdq::mx_dequantize<svdq::kMxFp4>(codes, sf, M, K, Y, ldy, stream);
 }
 
-extern "C" int svdq_dequantize_mxfp8(const uint8_t* codes, const uint8_t* sf, int64_t M, int64_t K, void* Y, int64_t ldy,
-                                     void* stream) {
+extern "C" int svdq_dequantize_mxfp8(const uint8_t* codes, const uint8_t* sf, int64_t M, int64_t K, void* Y,
+                                     int64_t ldy, void* stream) {
     return svdq::mx_dequantize<svdq::kMxFp8>(codes, sf, M, K, Y, ldy, stream);
 }

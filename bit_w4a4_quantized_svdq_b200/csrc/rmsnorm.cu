@@ -265,7 +265,8 @@ rmsnorm_mx_long_kernel(const NormArgs a) {
 // the memory's queue: 16384 x 5120 100 -> 95 us; with one round there is no next row to load
 // ahead (110 us).
 template <typename Kernel>
-int norm_launch(Kernel kern, const NormArgs& a, int threads, int rows_per_cta, int per_sm, int rounds, cudaStream_t st) {
+int norm_launch(Kernel kern, const NormArgs& a, int threads, int rows_per_cta, int per_sm, int rounds,
+                cudaStream_t st) {
     const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 148;
     const int64_t groups = (a.rows + rows_per_cta - 1) / rows_per_cta, wave = sms * per_sm;
     const int64_t waves = rounds ? std::max<int64_t>(1, (groups + wave * rounds / 2) / (wave * rounds)) : 1;

@@ -56,13 +56,13 @@ enum StoreSite : uint32_t {
     kSiteResidual = 12,       // residual weight
     kSiteGrid = 13,           // lambda grid: lambda, 1/lambda, scale
     kSiteBits = 14,           // bits lost
-    kSiteMxCodes = 15,        // MXFP8 quantiser: codes
-    kSiteMxSf = 16,           // MXFP8 quantiser: scale bytes
+    kSiteMxCodes = 15,        // MX quantisers and norms: codes
+    kSiteMxSf = 16,           // MX quantisers and norms: scale bytes
     kSiteCount = 17,
     // Numbered apart from the sites above.
     kSiteNormH = 32,          // RMS norm: the sum of input and residual
     kSiteMxValues = 33,       // MX read-back: bf16 values
-    kSiteLinearMx4 = 34,      // MXFP4 linear: plain stores of Y
+    kSiteLinearMx4 = 34,      // MXFP4 linear: Y (plain stores, or the origin of a TMA box)
     kSiteEnd = 35
 };
 

@@ -506,7 +506,8 @@ def _mx_outputs(out: Optional[dict], m: int, k: int, code_cols: int, dev) -> dic
     if nbytes == 0:
         raise ValueError("K must be a positive multiple of 128 and M at least 1")
     if out is None:
-        return dict(codes=_lib.out_empty((m, code_cols), torch.uint8, dev), sf=_lib.out_empty((nbytes,), torch.uint8, dev))
+        return dict(codes=_lib.out_empty((m, code_cols), torch.uint8, dev),
+                    sf=_lib.out_empty((nbytes,), torch.uint8, dev))
     _check_dense(out["codes"], (torch.uint8,), m * code_cols, "out['codes']")
     _check_dense(out["sf"], (torch.uint8,), nbytes, "out['sf']")
     return out
@@ -608,8 +609,8 @@ def _rmsnorm_mx(name: str, x, weight, residual, eps: float, per_byte: int, out, 
     q = _mx_outputs(out, m, k, k // per_byte, x.device)
     codes, sf = q["codes"], q["sf"]
     _lib.check(name, getattr(lib, name)(
-        x.data_ptr(), m, k, _row_stride(x, "x"), r_ptr, ldr, weight.data_ptr(), 1 if weight.dtype is torch.float32 else 0,
-        eps, h_ptr, ldh, codes.data_ptr(), sf.data_ptr(), _stream(stream)))
+        x.data_ptr(), m, k, _row_stride(x, "x"), r_ptr, ldr, weight.data_ptr(),
+        1 if weight.dtype is torch.float32 else 0, eps, h_ptr, ldh, codes.data_ptr(), sf.data_ptr(), _stream(stream)))
     return dict(codes=codes, sf=sf, h=h)
 
 
