@@ -9,9 +9,9 @@
 // that are not there.
 // A CTA owns one block of 128 weight rows and a slice of K; the slices of one block are a
 // cluster, whose partial sums meet over distributed shared memory in rank order (no
-// workspace, no atomics: bitwise repeatable).  One row, 5120 -> 5120: 5.3 us (14 MB; 2.1 us
+// workspace, no atomics: bitwise repeatable).  One row, 5120 -> 5120: 5.5 us (14 MB; 2.1 us
 // at the copy rate, and 3.7 us is what the smallest such call takes: launch, set-up, two
-// cluster barriers); 29 rows, 5120 -> 15360: 8.8 us, 4.9 TB/s.
+// cluster barriers); 29 rows, 5120 -> 15360: 8.9 us, 4.8 TB/s.
 //
 // More rows (linear_mx4_pair_kernel): persistent pairs of CTAs walk 256 x 256 tiles
 // (256 x 128 where that costs no further wave) with cta_group::2 MMAs, each CTA loading half

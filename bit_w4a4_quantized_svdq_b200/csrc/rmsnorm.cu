@@ -17,7 +17,7 @@
 // the current one is reduced; the weight is read once per CTA.  Rows from M to the
 // layout's 128-row padding only write their zero scales.
 //   16384 x 5120 with residual: into MXFP8 95-97 us (6.1 TB/s; a plain copy 6.5), into
-//   MXFP4 92; 4096 x 5120 27 us; one row 2.5 us; 16384 x 20480 (two passes) 453-477 us.
+//   MXFP4 92; 4096 x 5120 27 us; one row 3.1 us; 16384 x 20480 (two passes) 453-477 us.
 //   Without the next row's loads ahead 16384 x 5120 takes 132 us.
 #include <algorithm>
 #include <cfloat>
